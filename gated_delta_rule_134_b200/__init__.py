@@ -1,4 +1,7 @@
-"""KDA (fine-grained gated delta rule) for B200: Python binding of libkda.so.
+"""KDA (fine-grained gated delta rule) for B200: Python binding of libkda.so,
+with the other layers of a hybrid stack beside it: the gated linear recurrence,
+the query/key norm with the position rotation, and the attention of one new
+token over a paged key-value cache.
 
 Argument marshalling only: every step of the computation runs in the CUDA
 kernels behind the C ABI declared in include/kda.h. PyTorch provides device
@@ -11,7 +14,9 @@ import ctypes
 import os
 
 __all__ = ["load", "chunk_fwd", "chunk_fwd_varlen", "chunk_bwd", "chunk_fwd_noalloc", "noalloc_status", "decode_step",
-           "workspace_size", "workspace_status", "chunk_fwd_timeout_test", "KDAError", "library_path", "STATUS"]
+           "workspace_size", "workspace_status", "chunk_fwd_timeout_test", "KDAError", "library_path", "STATUS",
+           "recurrence_fwd", "recurrence_bwd", "recurrence_step", "qk_norm_rope", "qk_norm_rope_bwd", "attn_decode",
+           "attn_decode_workspace_size"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libkda.so")
@@ -23,6 +28,7 @@ _ALGO = {"auto": 0, "simt": 1, "tc": 2, "tc_scan": 3}
 # Variant switches (include/kda.h): gate "channel" = log_alpha [.., dk], "scalar" =
 # one per token and head, "none" = no decay (log_alpha may be None).
 GATES = {"channel": 0, "scalar": 1, "none": 2}
+NORMS = {"l2": 0, "rms": 1}
 
 
 class KDAError(RuntimeError):
@@ -84,6 +90,23 @@ def load(build_if_stale: bool = True):
     lib.kda_chunk_bwd_ex.restype = I
     lib.kda_chunk_bwd_workspace_size_ex.argtypes = [I] * 6
     lib.kda_chunk_bwd_workspace_size_ex.restype = Z
+    F, L = ctypes.c_float, ctypes.c_longlong
+    lib.kda_recurrence_fwd.argtypes = [P] * 6 + [I] * 4 + [P]
+    lib.kda_recurrence_fwd.restype = I
+    lib.kda_recurrence_bwd.argtypes = [P] * 9 + [I] * 4 + [P]
+    lib.kda_recurrence_bwd.restype = I
+    lib.kda_recurrence_step.argtypes = [P] * 5 + [I] * 3 + [P]
+    lib.kda_recurrence_step.restype = I
+    lib.kda_qk_norm_rope.argtypes = [P] * 7 + [I] + [P] * 2 + [I] * 6 + [L] * 4 + [I, F, F, I, I, P]
+    lib.kda_qk_norm_rope.restype = I
+    lib.kda_qk_norm_rope_bwd_workspace_size.argtypes = [I] * 4
+    lib.kda_qk_norm_rope_bwd_workspace_size.restype = Z
+    lib.kda_qk_norm_rope_bwd.argtypes = [P] * 9 + [I] + [P] * 4 + [I] * 6 + [L] * 4 + [I, F, F, I, I, P, Z, P]
+    lib.kda_qk_norm_rope_bwd.restype = I
+    lib.kda_attn_decode_workspace_size.argtypes = [I] * 4
+    lib.kda_attn_decode_workspace_size.restype = Z
+    lib.kda_attn_decode.argtypes = [P] * 9 + [I] * 8 + [F, I, P, Z, P]
+    lib.kda_attn_decode.restype = I
     _lib = lib
     return lib
 
@@ -392,3 +415,290 @@ def noalloc_status(device=None, stream=None) -> int:
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     with _on(dev):
         return int(load().kda_noalloc_status(_stream(stream, dev)))
+
+
+# ---------------------------------------------------------------- gated linear recurrence
+
+
+def _recurrence_sizes(log_alpha, cu_seqlens):
+    """(N, T, D) of a dense [B,T,D] or a packed [T,D] batch."""
+    import torch
+    if cu_seqlens is None:
+        if log_alpha.dim() != 3:
+            raise ValueError(f"log_alpha: expected [B,T,D], got {tuple(log_alpha.shape)}")
+        return tuple(log_alpha.shape)
+    if log_alpha.dim() != 2:
+        raise ValueError(f"log_alpha: expected packed [total_T,D], got {tuple(log_alpha.shape)}")
+    N = cu_seqlens.numel() - 1
+    if N < 0:
+        raise ValueError("cu_seqlens: expected N + 1 offsets")
+    _need(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32, log_alpha.device)
+    return N, log_alpha.shape[0], log_alpha.shape[1]
+
+
+def recurrence_fwd(log_alpha, x, h0=None, *, cu_seqlens=None, output_final_state: bool = True, h=None, h_T=None,
+                   stream=None):
+    """kda_recurrence_fwd: h_t = exp(log_alpha_t) h_{t-1} + x_t per channel.
+
+    log_alpha, x: [B,T,D], or packed [total_T,D] with cu_seqlens int32 [N+1];
+    both float32 or both bfloat16. h0: [B or N,D] float32 or None (zero).
+    Returns (h, h_T): h like x, h_T [B or N,D] float32 (None when
+    output_final_state is False). h may be x, h_T may be h0."""
+    import torch
+    lib = load()
+    N, T, D = _recurrence_sizes(log_alpha, cu_seqlens)
+    dt, dev, shape = log_alpha.dtype, log_alpha.device, log_alpha.shape
+    dts = _dtype_of(log_alpha)
+    _need(log_alpha, "log_alpha", shape, dt, dev)
+    _need(x, "x", shape, dt, dev)
+    if h0 is not None:
+        _need(h0, "h0", (N, D), torch.float32, dev)
+    if h is None:
+        h = torch.empty_like(x)
+    else:
+        _need(h, "h", shape, dt, dev)
+    if h_T is not None:
+        _need(h_T, "h_T", (N, D), torch.float32, dev)
+    elif output_final_state:
+        h_T = torch.empty(N, D, dtype=torch.float32, device=dev)
+    with _on(dev):
+        code = lib.kda_recurrence_fwd(_ptr(log_alpha), _ptr(x), _ptr(h0), _ptr(h), _ptr(h_T), _ptr(cu_seqlens),
+                                      N, T, D, _DTYPE[dts], _stream(stream, dev))
+    _check("kda_recurrence_fwd", code)
+    return h, h_T
+
+
+def recurrence_bwd(log_alpha, h, h0, dh, dh_T=None, *, cu_seqlens=None, want_dh0: bool = True, stream=None) -> dict:
+    """kda_recurrence_bwd: gradients of a loss with dL/dh = dh and dL/dh_T =
+    dh_T ([B or N,D] float32 or None). log_alpha, h0, cu_seqlens as for
+    recurrence_fwd, h its output. Returns dict dx, dlog_alpha, dh0 (None
+    unless want_dh0)."""
+    import torch
+    lib = load()
+    N, T, D = _recurrence_sizes(log_alpha, cu_seqlens)
+    dt, dev, shape = log_alpha.dtype, log_alpha.device, log_alpha.shape
+    dts = _dtype_of(log_alpha)
+    _need(log_alpha, "log_alpha", shape, dt, dev)
+    _need(h, "h", shape, dt, dev)
+    _need(dh, "dh", shape, dt, dev)
+    if h0 is not None:
+        _need(h0, "h0", (N, D), torch.float32, dev)
+    if dh_T is not None:
+        _need(dh_T, "dh_T", (N, D), torch.float32, dev)
+    g = {"dx": torch.empty_like(dh), "dlog_alpha": torch.empty_like(log_alpha),
+         "dh0": torch.empty(N, D, dtype=torch.float32, device=dev) if want_dh0 else None}
+    with _on(dev):
+        code = lib.kda_recurrence_bwd(_ptr(log_alpha), _ptr(h), _ptr(h0), _ptr(dh), _ptr(dh_T), _ptr(g["dx"]),
+                                      _ptr(g["dlog_alpha"]), _ptr(g["dh0"]), _ptr(cu_seqlens), N, T, D, _DTYPE[dts],
+                                      _stream(stream, dev))
+    _check("kda_recurrence_bwd", code)
+    return g
+
+
+def recurrence_step(log_alpha, x, h, *, h_out=None, y=None, stream=None):
+    """kda_recurrence_step: one token per sequence. log_alpha, x: [N,D]; h
+    [N,D] float32. h_out defaults to h (in-place update). Returns (y, h_out)
+    with y = h_out in the inputs' dtype."""
+    import torch
+    lib = load()
+    if log_alpha.dim() != 2:
+        raise ValueError(f"log_alpha: expected [N,D], got {tuple(log_alpha.shape)}")
+    N, D = log_alpha.shape
+    dt, dev = log_alpha.dtype, log_alpha.device
+    dts = _dtype_of(log_alpha)
+    _need(log_alpha, "log_alpha", (N, D), dt, dev)
+    _need(x, "x", (N, D), dt, dev)
+    _need(h, "h", (N, D), torch.float32, dev)
+    if h_out is None:
+        h_out = h
+    else:
+        _need(h_out, "h_out", (N, D), torch.float32, dev)
+    if y is None:
+        y = torch.empty_like(x)
+    else:
+        _need(y, "y", (N, D), dt, dev)
+    with _on(dev):
+        code = lib.kda_recurrence_step(_ptr(log_alpha), _ptr(x), _ptr(h), _ptr(h_out), _ptr(y), N, D, _DTYPE[dts],
+                                       _stream(stream, dev))
+    _check("kda_recurrence_step", code)
+    return y, h_out
+
+
+# ---------------------------------------------------------------- query/key norm and rotation
+
+
+def _heads_view(t, name, lead, d, dt, dev):
+    """t [*lead, H, d] as [n, H, d] without a copy: any head and token strides, channels contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor (this library has no CPU path)")
+    if t.device != dev or t.dtype != dt or tuple(t.shape[:-2]) != tuple(lead) or t.shape[-1] != d:
+        raise ValueError(f"{name}: expected {dt} {tuple(lead) + ('heads', d)} on {dev}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    if t.numel() and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the channels of a head must be contiguous")
+    if t.dim() == 3:
+        return t
+    n = 1
+    for s in lead:
+        n *= s
+    try:
+        return t.view(n, t.shape[-2], d)
+    except RuntimeError:
+        raise ValueError(f"{name}: the leading dimensions {tuple(lead)} must have one common stride") from None
+
+
+def _qk_args(q, k, q_weight, k_weight, cos, sin, positions, norm):
+    """Checks what the two directions share; (q view, k view, n, Hq, Hk, d, rot, max_pos, pos_bytes)."""
+    import torch
+    if norm not in NORMS:
+        raise ValueError(f"norm must be one of {sorted(NORMS)}")
+    if q.dim() < 3 or k.dim() != q.dim():
+        raise ValueError(f"q, k: expected [..., tokens, heads, d], got {tuple(q.shape)} and {tuple(k.shape)}")
+    dt, dev, lead, d = q.dtype, q.device, q.shape[:-2], q.shape[-1]
+    qv, kv = _heads_view(q, "q", lead, d, dt, dev), _heads_view(k, "k", lead, d, dt, dev)
+    n = qv.shape[0]
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _need(w, name, (d,), dt, dev)
+    rot = max_pos = pos_bytes = 0
+    if positions is not None:
+        if cos is None or sin is None:
+            raise ValueError("positions need the cos and sin tables")
+        if cos.dim() != 2:
+            raise ValueError(f"cos: expected [max_pos, rot/2], got {tuple(cos.shape)}")
+        max_pos, rot = cos.shape[0], 2 * cos.shape[1]
+        _need(cos, "cos", (max_pos, rot // 2), torch.float32, dev)
+        _need(sin, "sin", (max_pos, rot // 2), torch.float32, dev)
+        if positions.dtype not in (torch.int32, torch.int64):
+            raise TypeError(f"positions: expected int32 or int64, got {positions.dtype}")
+        pos_bytes = positions.element_size()
+        if positions.numel() != n:
+            raise ValueError(f"positions: expected one per token ({n}), got {tuple(positions.shape)}")
+        _need(positions, "positions", positions.shape, positions.dtype, dev)
+    return qv, kv, n, qv.shape[1], kv.shape[1], d, rot, max_pos, pos_bytes
+
+
+def qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positions=None, *, norm: str = "rms",
+                 eps: float = 1e-6, q_scale: float = 1.0, interleaved: bool = False, q_out=None, k_out=None,
+                 stream=None):
+    """kda_qk_norm_rope: queries and keys normalised per head and rotated by
+    position in one pass.
+
+    q: [..., Hq, d], k: [..., Hk, d] with the same leading dimensions, both
+    float32 or both bfloat16; slices of a fused projection are read in place
+    (channels contiguous, other strides multiples of 16 bytes). q_weight,
+    k_weight: [d] or None. positions: int32 or int64, one per token, or None
+    (no rotation); cos, sin: [max_pos, rot/2] float32. norm: "l2" or "rms".
+    Returns contiguous (q_out, k_out); q_out may be q where q is contiguous."""
+    import torch
+    lib = load()
+    dts = _dtype_of(q)
+    qv, kv, n, Hq, Hk, d, rot, max_pos, pos_bytes = _qk_args(q, k, q_weight, k_weight, cos, sin, positions, norm)
+    dt, dev = q.dtype, q.device
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=dt, device=dev)
+    else:
+        _need(q_out, "q_out", q.shape, dt, dev)
+    if k_out is None:
+        k_out = torch.empty(k.shape, dtype=dt, device=dev)
+    else:
+        _need(k_out, "k_out", k.shape, dt, dev)
+    with _on(dev):
+        code = lib.kda_qk_norm_rope(_ptr(qv), _ptr(kv), _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin),
+                                    _ptr(positions), pos_bytes, _ptr(q_out), _ptr(k_out), n, Hq, Hk, d, rot, max_pos,
+                                    qv.stride(0), qv.stride(1), kv.stride(0), kv.stride(1), NORMS[norm], eps, q_scale,
+                                    int(bool(interleaved)), _DTYPE[dts], _stream(stream, dev))
+    _check("kda_qk_norm_rope", code)
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, cos=None, sin=None, positions=None, *,
+                     norm: str = "rms", eps: float = 1e-6, q_scale: float = 1.0, interleaved: bool = False,
+                     workspace=None, stream=None) -> dict:
+    """kda_qk_norm_rope_bwd: gradients of a loss with dL/dq_out = dq_out and
+    dL/dk_out = dk_out (contiguous, shaped like q and k); the other arguments
+    as for qk_norm_rope. Returns dict dq, dk (contiguous), dq_weight,
+    dk_weight (float32 [d]; None without a weight)."""
+    import torch
+    lib = load()
+    dts = _dtype_of(q)
+    qv, kv, n, Hq, Hk, d, rot, max_pos, pos_bytes = _qk_args(q, k, q_weight, k_weight, cos, sin, positions, norm)
+    dt, dev = q.dtype, q.device
+    _need(dq_out, "dq_out", q.shape, dt, dev)
+    _need(dk_out, "dk_out", k.shape, dt, dev)
+    g = {"dq": torch.empty(q.shape, dtype=dt, device=dev), "dk": torch.empty(k.shape, dtype=dt, device=dev),
+         "dq_weight": None if q_weight is None else torch.empty(d, dtype=torch.float32, device=dev),
+         "dk_weight": None if k_weight is None else torch.empty(d, dtype=torch.float32, device=dev)}
+    if workspace is None and (q_weight is not None or k_weight is not None):
+        workspace = torch.empty(int(lib.kda_qk_norm_rope_bwd_workspace_size(n, Hq, Hk, d)), dtype=torch.uint8,
+                                device=dev)
+    ws_len = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    with _on(dev):
+        code = lib.kda_qk_norm_rope_bwd(_ptr(dq_out), _ptr(dk_out), _ptr(qv), _ptr(kv), _ptr(q_weight),
+                                        _ptr(k_weight), _ptr(cos), _ptr(sin), _ptr(positions), pos_bytes,
+                                        _ptr(g["dq"]), _ptr(g["dk"]), _ptr(g["dq_weight"]), _ptr(g["dk_weight"]), n,
+                                        Hq, Hk, d, rot, max_pos, qv.stride(0), qv.stride(1), kv.stride(0),
+                                        kv.stride(1), NORMS[norm], eps, q_scale, int(bool(interleaved)), _DTYPE[dts],
+                                        _ptr(workspace), ws_len, _stream(stream, dev))
+    _check("kda_qk_norm_rope_bwd", code)
+    return g
+
+
+# ---------------------------------------------------------------- paged decode attention
+
+
+def attn_decode_workspace_size(N, Hq, Hk, d) -> int:
+    return int(load().kda_attn_decode_workspace_size(N, Hq, Hk, d))
+
+
+def attn_decode(q, k_cache, v_cache, page_table, seq_lens, *, k=None, v=None, scale=None, window: int = 0, o=None,
+                lse=None, return_lse: bool = False, workspace=None, stream=None):
+    """kda_attn_decode: one new token per sequence over a paged key-value cache.
+
+    q: [N,Hq,d]; k, v: [N,Hk,d], the new token's key and value, put into the
+    cache at position seq_lens[n] (or both None); k_cache, v_cache:
+    [n_pages,Hk,page_size,d], updated in place; page_table: int32
+    [N,max_pages]; seq_lens: int32 [N], positions held before the call,
+    negative for rows of a padded batch. scale defaults to d**-0.5; window > 0
+    attends to the last `window` positions only. Returns o [N,Hq,d], or (o,
+    lse) with lse [N,Hq] float32 when return_lse is set or lse is given."""
+    import torch
+    lib = load()
+    if q.dim() != 3 or k_cache.dim() != 4 or page_table.dim() != 2:
+        raise ValueError(f"expected q [N,Hq,d], k_cache [n_pages,Hk,page_size,d], page_table [N,max_pages], got "
+                         f"{tuple(q.shape)}, {tuple(k_cache.shape)}, {tuple(page_table.shape)}")
+    N, Hq, d = q.shape
+    n_pages, Hk, page_size, _ = k_cache.shape
+    max_pages = page_table.shape[1]
+    dt, dev = q.dtype, q.device
+    dts = _dtype_of(q)
+    _need(q, "q", (N, Hq, d), dt, dev)
+    _need(k_cache, "k_cache", (n_pages, Hk, page_size, d), dt, dev)
+    _need(v_cache, "v_cache", (n_pages, Hk, page_size, d), dt, dev)
+    _need(page_table, "page_table", (N, max_pages), torch.int32, dev)
+    _need(seq_lens, "seq_lens", (N,), torch.int32, dev)
+    if (k is None) != (v is None):
+        raise ValueError("k and v: give both or neither")
+    if k is not None:
+        _need(k, "k", (N, Hk, d), dt, dev)
+        _need(v, "v", (N, Hk, d), dt, dev)
+    if o is None:
+        o = torch.empty(N, Hq, d, dtype=dt, device=dev)
+    else:
+        _need(o, "o", (N, Hq, d), dt, dev)
+    if lse is not None:
+        _need(lse, "lse", (N, Hq), torch.float32, dev)
+        return_lse = True
+    elif return_lse:
+        lse = torch.empty(N, Hq, dtype=torch.float32, device=dev)
+    ws_bytes = int(lib.kda_attn_decode_workspace_size(N, Hq, Hk, d))
+    if ws_bytes and workspace is None:
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    ws_len = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    with _on(dev):
+        code = lib.kda_attn_decode(_ptr(q), _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(page_table),
+                                   _ptr(seq_lens), _ptr(o), _ptr(lse), N, Hq, Hk, d, n_pages, page_size, max_pages,
+                                   int(window), d ** -0.5 if scale is None else scale, _DTYPE[dts], _ptr(workspace),
+                                   ws_len, _stream(stream, dev))
+    _check("kda_attn_decode", code)
+    return (o, lse) if return_lse else o

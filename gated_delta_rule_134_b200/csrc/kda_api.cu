@@ -250,4 +250,175 @@ kda_status_t kda_chunk_bwd_ex(const void* q, const void* k, const void* v, const
     return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
+// ---------------------------------------------------------------- gated linear recurrence
+
+static bool dtype_ok(kda_dtype_t dtype) { return dtype == KDA_F32 || dtype == KDA_BF16; }
+static bool good(const void* p) { return p != nullptr && aligned16(p); }
+
+static kda_status_t check_recurrence(const kda::RecurrenceArgs& a, kda_dtype_t dtype, bool bwd) {
+    if (a.N < 0 || a.T < 0 || a.D < 1) return KDA_ERR_INVALID_ARG;
+    if (!dtype_ok(dtype)) return KDA_ERR_INVALID_ARG;
+    if ((long long)a.N * ((a.D + 31) / 32) > 0x3ffffffLL) return KDA_ERR_INVALID_ARG;  // grid limit, clusters included
+    if (a.cu_seqlens && (reinterpret_cast<uintptr_t>(a.cu_seqlens) & 3u) != 0) return KDA_ERR_INVALID_ARG;
+    if ((long long)a.N * a.T > 0) {
+        if (!good(a.log_alpha) || !good(a.x) || !good(a.out)) return KDA_ERR_INVALID_ARG;
+        if (bwd && (!good(a.h_fwd) || !good(a.out_la))) return KDA_ERR_INVALID_ARG;
+    }
+    const float* opt[] = {a.state0, a.h0, a.state_end};
+    for (const float* p : opt)
+        if (p && !aligned16(p)) return KDA_ERR_INVALID_ARG;
+    return KDA_OK;
+}
+
+kda_status_t kda_recurrence_fwd(const void* log_alpha, const void* x, const float* h0, void* h, float* h_T,
+                                const int* cu_seqlens, int N, int T, int D, kda_dtype_t dtype, void* stream) {
+    kda::RecurrenceArgs a{};
+    a.log_alpha = log_alpha; a.x = x; a.state0 = h0; a.out = h; a.state_end = h_T; a.cu_seqlens = cu_seqlens;
+    a.N = N; a.T = T; a.D = D; a.bf16 = dtype == KDA_BF16;
+    const kda_status_t st = check_recurrence(a, dtype, false);
+    if (st != KDA_OK) return st;
+    if (N == 0) return KDA_OK;
+    return kda::launch_recurrence_fwd(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+kda_status_t kda_recurrence_bwd(const void* log_alpha, const void* h, const float* h0, const void* d_h,
+                                const float* d_h_T, void* d_x, void* d_log_alpha, float* d_h0,
+                                const int* cu_seqlens, int N, int T, int D, kda_dtype_t dtype, void* stream) {
+    kda::RecurrenceArgs a{};
+    a.log_alpha = log_alpha; a.x = d_h; a.h_fwd = h; a.h0 = h0; a.state0 = d_h_T; a.out = d_x;
+    a.out_la = d_log_alpha; a.state_end = d_h0; a.cu_seqlens = cu_seqlens;
+    a.N = N; a.T = T; a.D = D; a.bf16 = dtype == KDA_BF16;
+    const kda_status_t st = check_recurrence(a, dtype, true);
+    if (st != KDA_OK) return st;
+    if (N == 0) return KDA_OK;
+    return kda::launch_recurrence_bwd(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+kda_status_t kda_recurrence_step(const void* log_alpha, const void* x, const float* h_in, float* h_out, void* y,
+                                 int N, int D, kda_dtype_t dtype, void* stream) {
+    if (N < 0 || D < 1 || !dtype_ok(dtype)) return KDA_ERR_INVALID_ARG;
+    if (N == 0) return KDA_OK;
+    const void* req[] = {log_alpha, x, h_in, h_out, y};
+    for (const void* p : req)
+        if (!good(p)) return KDA_ERR_INVALID_ARG;
+    const cudaError_t err = kda::launch_recurrence_step(log_alpha, x, h_in, h_out, y, (long long)N * D,
+                                                        dtype == KDA_BF16, static_cast<cudaStream_t>(stream));
+    return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------- query/key norm and rotation
+
+static kda_status_t check_qk(const kda::QkArgs& a, kda_dtype_t dtype, kda_norm_t norm, bool bwd) {
+    if (a.n < 0 || a.Hq < 0 || a.Hk < 0 || !dtype_ok(dtype)) return KDA_ERR_INVALID_ARG;
+    if (a.Hq > 65535 || a.Hk > 65535) return KDA_ERR_INVALID_ARG;
+    if (norm != KDA_NORM_L2 && norm != KDA_NORM_RMS) return KDA_ERR_INVALID_ARG;
+    if (a.interleaved != 0 && a.interleaved != 1) return KDA_ERR_INVALID_ARG;
+    if (!(a.eps > 0.f) || a.eps > 3.0e38f) return KDA_ERR_INVALID_ARG;
+    if (a.d < 8 || a.d > 256 || a.d % 8 != 0) return KDA_ERR_UNSUPPORTED;
+    if (a.positions) {
+        if (a.pos_bytes != 4 && a.pos_bytes != 8) return KDA_ERR_INVALID_ARG;
+        if ((reinterpret_cast<uintptr_t>(a.positions) & (uintptr_t)(a.pos_bytes - 1)) != 0) return KDA_ERR_INVALID_ARG;
+        if (a.rot < 16 || a.rot > a.d || a.rot % 16 != 0) return KDA_ERR_UNSUPPORTED;
+        if (a.max_pos < 1 || !good(a.cos) || !good(a.sin)) return KDA_ERR_INVALID_ARG;
+    }
+    if (a.n == 0) return KDA_OK;
+    const long long unit = dtype == KDA_BF16 ? 8 : 4;  // elements of 16 bytes
+    if (a.Hq > 0) {
+        if (!good(a.q) || !good(a.q_out) || (bwd && !good(a.d_q_out))) return KDA_ERR_INVALID_ARG;
+        if (a.q_stride_t % unit != 0 || a.q_stride_h % unit != 0) return KDA_ERR_INVALID_ARG;
+    }
+    if (a.Hk > 0) {
+        if (!good(a.k) || !good(a.k_out) || (bwd && !good(a.d_k_out))) return KDA_ERR_INVALID_ARG;
+        if (a.k_stride_t % unit != 0 || a.k_stride_h % unit != 0) return KDA_ERR_INVALID_ARG;
+    }
+    const void* opt[] = {a.q_weight, a.k_weight, a.d_q_weight, a.d_k_weight};
+    for (const void* p : opt)
+        if (p && !aligned16(p)) return KDA_ERR_INVALID_ARG;
+    return KDA_OK;
+}
+
+kda_status_t kda_qk_norm_rope(const void* q, const void* k, const void* q_weight, const void* k_weight,
+                              const float* cos, const float* sin, const void* positions, int pos_bytes, void* q_out,
+                              void* k_out, int n, int Hq, int Hk, int d, int rot, int max_pos, long long q_stride_t,
+                              long long q_stride_h, long long k_stride_t, long long k_stride_h, kda_norm_t norm,
+                              float eps, float q_scale, int interleaved, kda_dtype_t dtype, void* stream) {
+    kda::QkArgs a{};
+    a.q = q; a.k = k; a.q_weight = q_weight; a.k_weight = k_weight; a.cos = cos; a.sin = sin;
+    a.positions = positions; a.pos_bytes = pos_bytes; a.q_out = q_out; a.k_out = k_out;
+    a.n = n; a.Hq = Hq; a.Hk = Hk; a.d = d; a.rot = positions ? rot : 0; a.max_pos = max_pos;
+    a.q_stride_t = q_stride_t; a.q_stride_h = q_stride_h; a.k_stride_t = k_stride_t; a.k_stride_h = k_stride_h;
+    a.norm = (int)norm; a.eps = eps; a.q_scale = q_scale; a.interleaved = interleaved; a.bf16 = dtype == KDA_BF16;
+    const kda_status_t st = check_qk(a, dtype, norm, false);
+    if (st != KDA_OK) return st;
+    if (n == 0 || Hq + Hk == 0) return KDA_OK;
+    return kda::launch_qk_norm_rope(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+size_t kda_qk_norm_rope_bwd_workspace_size(int n, int Hq, int Hk, int d) {
+    if (n < 0 || Hq < 0 || Hk < 0 || d < 8 || d > 256 || d % 8 != 0) return 0;
+    return kda::qk_norm_rope_bwd_workspace_bytes(n, Hq, Hk, d);
+}
+
+kda_status_t kda_qk_norm_rope_bwd(const void* d_q_out, const void* d_k_out, const void* q, const void* k,
+                                  const void* q_weight, const void* k_weight, const float* cos, const float* sin,
+                                  const void* positions, int pos_bytes, void* d_q, void* d_k, float* d_q_weight,
+                                  float* d_k_weight, int n, int Hq, int Hk, int d, int rot, int max_pos,
+                                  long long q_stride_t, long long q_stride_h, long long k_stride_t,
+                                  long long k_stride_h, kda_norm_t norm, float eps, float q_scale, int interleaved,
+                                  kda_dtype_t dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    kda::QkArgs a{};
+    a.q = q; a.k = k; a.q_weight = q_weight; a.k_weight = k_weight; a.cos = cos; a.sin = sin;
+    a.positions = positions; a.pos_bytes = pos_bytes; a.d_q_out = d_q_out; a.d_k_out = d_k_out;
+    a.q_out = d_q; a.k_out = d_k; a.d_q_weight = d_q_weight; a.d_k_weight = d_k_weight;
+    a.n = n; a.Hq = Hq; a.Hk = Hk; a.d = d; a.rot = positions ? rot : 0; a.max_pos = max_pos;
+    a.q_stride_t = q_stride_t; a.q_stride_h = q_stride_h; a.k_stride_t = k_stride_t; a.k_stride_h = k_stride_h;
+    a.norm = (int)norm; a.eps = eps; a.q_scale = q_scale; a.interleaved = interleaved; a.bf16 = dtype == KDA_BF16;
+    a.workspace = workspace;
+    const kda_status_t st = check_qk(a, dtype, norm, true);
+    if (st != KDA_OK) return st;
+    if (d_q_weight || d_k_weight) {
+        const size_t need = kda::qk_norm_rope_bwd_workspace_bytes(n, Hq, Hk, d);
+        if (need > 0 && (!good(workspace) || workspace_bytes < need)) return KDA_ERR_INVALID_ARG;
+    }
+    return kda::launch_qk_norm_rope_bwd(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------- paged decode attention
+
+static bool attn_heads_ok(int Hq, int Hk) { return Hk > 0 && Hq > 0 && Hq % Hk == 0; }
+
+size_t kda_attn_decode_workspace_size(int N, int Hq, int Hk, int d) {
+    if (N <= 0 || !attn_heads_ok(Hq, Hk) || (d != 64 && d != 128)) return 0;
+    return kda::attn_decode_workspace_bytes(N, Hq, Hk, d);
+}
+
+kda_status_t kda_attn_decode(const void* q, const void* k_new, const void* v_new, void* k_cache, void* v_cache,
+                             const int* page_table, const int* seq_lens, void* o, float* lse, int N, int Hq, int Hk,
+                             int d, int n_pages, int page_size, int max_pages, int window, float scale,
+                             kda_dtype_t dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    if (N < 0 || !attn_heads_ok(Hq, Hk) || n_pages < 0 || page_size < 1 || max_pages < 0 || window < 0)
+        return KDA_ERR_INVALID_ARG;
+    if (!dtype_ok(dtype) || !(scale == scale)) return KDA_ERR_INVALID_ARG;
+    if (d != 64 && d != 128) return KDA_ERR_UNSUPPORTED;
+    // positions, and the work items of all rows, are counted in int32
+    if ((long long)max_pages * page_size > 0x3fffffffLL || (long long)N * Hq > 0xffffffLL) return KDA_ERR_INVALID_ARG;
+    if (N == 0) return KDA_OK;
+    if (!good(q) || !good(o)) return KDA_ERR_INVALID_ARG;
+    if ((k_new == nullptr) != (v_new == nullptr)) return KDA_ERR_INVALID_ARG;
+    if (k_new && (!aligned16(k_new) || !aligned16(v_new))) return KDA_ERR_INVALID_ARG;
+    if (n_pages > 0 && (!good(k_cache) || !good(v_cache))) return KDA_ERR_INVALID_ARG;
+    if (seq_lens == nullptr || (reinterpret_cast<uintptr_t>(seq_lens) & 3u) != 0) return KDA_ERR_INVALID_ARG;
+    if (max_pages > 0 && (page_table == nullptr || (reinterpret_cast<uintptr_t>(page_table) & 3u) != 0))
+        return KDA_ERR_INVALID_ARG;
+    if (lse && (reinterpret_cast<uintptr_t>(lse) & 3u) != 0) return KDA_ERR_INVALID_ARG;
+    const size_t need = kda::attn_decode_workspace_bytes(N, Hq, Hk, d);
+    if (need > 0 && (!good(workspace) || workspace_bytes < need)) return KDA_ERR_INVALID_ARG;
+    kda::AttnDecodeArgs a{};
+    a.q = q; a.k_new = k_new; a.v_new = v_new; a.k_cache = k_cache; a.v_cache = v_cache;
+    a.page_table = page_table; a.seq_lens = seq_lens; a.o = o; a.lse = lse;
+    a.N = N; a.Hq = Hq; a.Hk = Hk; a.d = d; a.n_pages = n_pages; a.page_size = page_size; a.max_pages = max_pages;
+    a.window = window; a.scale = scale; a.bf16 = dtype == KDA_BF16; a.workspace = workspace;
+    return kda::launch_attn_decode(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
 }  // extern "C"

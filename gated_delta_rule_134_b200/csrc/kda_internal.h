@@ -63,4 +63,56 @@ struct BwdArgs {
 size_t chunk_bwd_workspace_bytes(int B, int T, int H, int d, int mode);
 cudaError_t launch_chunk_bwd(const BwdArgs& a, cudaStream_t stream);
 
+// Gated linear recurrence h_t = exp(log_alpha_t) h_{t-1} + x_t. Dense [N, T, D],
+// or packed [T, D] with cu_seqlens [N + 1].
+struct RecurrenceArgs {
+    const void *log_alpha, *x;  // backward: x is the gradient of h
+    const void* h_fwd;          // backward: the forward pass's h
+    const float *state0;        // forward: h0; backward: d_h_T (the state the reverse recurrence starts from)
+    const float* h0;            // backward: h0, the h_{t-1} of a first token
+    void *out, *out_la;         // forward: h; backward: d_x, d_log_alpha
+    float* state_end;           // forward: h_T; backward: d_h0
+    const int* cu_seqlens;
+    int N, T, D, bf16;
+};
+cudaError_t launch_recurrence_fwd(const RecurrenceArgs& a, cudaStream_t stream);
+cudaError_t launch_recurrence_bwd(const RecurrenceArgs& a, cudaStream_t stream);
+cudaError_t launch_recurrence_step(const void* la, const void* x, const float* h_in, float* h_out, void* y,
+                                   long long cells, int bf16, cudaStream_t stream);
+
+// Per-head norm of queries and keys with the position rotation.
+struct QkArgs {
+    const void *q, *k, *q_weight, *k_weight;
+    const float *cos, *sin;
+    const void* positions;  // NULL: no rotation
+    int pos_bytes;
+    const void *d_q_out, *d_k_out;  // backward only
+    void *q_out, *k_out;            // backward: d_q, d_k
+    float *d_q_weight, *d_k_weight;
+    int n, Hq, Hk, d, rot, max_pos;
+    long long q_stride_t, q_stride_h, k_stride_t, k_stride_h;
+    int norm;
+    float eps, q_scale;
+    int interleaved, bf16;
+    void* workspace;
+};
+size_t qk_norm_rope_bwd_workspace_bytes(int n, int Hq, int Hk, int d);
+cudaError_t launch_qk_norm_rope(const QkArgs& a, cudaStream_t stream);
+cudaError_t launch_qk_norm_rope_bwd(const QkArgs& a, cudaStream_t stream);
+
+// One new token's attention over a paged key-value cache.
+struct AttnDecodeArgs {
+    const void *q, *k_new, *v_new;
+    void *k_cache, *v_cache;
+    const int *page_table, *seq_lens;
+    void* o;
+    float* lse;
+    int N, Hq, Hk, d, n_pages, page_size, max_pages, window;
+    float scale;
+    int bf16;
+    void* workspace;
+};
+size_t attn_decode_workspace_bytes(int N, int Hq, int Hk, int d);
+cudaError_t launch_attn_decode(const AttnDecodeArgs& a, cudaStream_t stream);
+
 }  // namespace kda

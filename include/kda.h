@@ -3,7 +3,10 @@
  * prefill (dense or packed batches, optional chunk-parallel segment scan), its
  * backward pass, and the single-token decode step on NVIDIA B200 (sm_100a);
  * the delta-rule and gated-linear-attention variants run through the same
- * calls.
+ * calls. Beside them, what the other layers of a hybrid stack need: the gated
+ * linear recurrence (kda_recurrence_*), the per-head norm of queries and keys
+ * with the position rotation (kda_qk_norm_rope, _bwd) and the attention of one
+ * new token over a paged key-value cache (kda_attn_decode).
  *
  * The operation (pages: "Decoding Hybrid Attention Architectures", section
  * 3.4 and its variant table; "Technical Analysis ... Novel Hybrid Linear
@@ -329,6 +332,158 @@ kda_status_t kda_chunk_fwd_noalloc(const void *q, const void *k, const void *v, 
  * same way as the calls themselves when they overlap on the GPU.
  */
 kda_status_t kda_noalloc_status(void *stream);
+
+/*
+ * Gated linear recurrence (elementwise; the vector-state layer of a hybrid
+ * stack): per sequence and channel, token by token,
+ *
+ *     h_t = exp(log_alpha_t) * h_{t-1} + x_t
+ *
+ *   log_alpha, x    : [N, T, D]       dtype (no activation is applied; meant
+ *                                     to be <= 0, -INFINITY resets a channel)
+ *   h0              : [N, D]          float, initial state; NULL means zero
+ *   h               : [N, T, D]       dtype, written (may equal x)
+ *   h_T             : [N, D]          float, final state before its rounding
+ *                                     to dtype; NULL means not written (may
+ *                                     equal h0: read fully before written)
+ *   cu_seqlens      : NULL for the dense batch above. Else N packed sequences:
+ *                     log_alpha, x, h are [T, D], T the total token count, and
+ *                     cu_seqlens is DEVICE int32 [N + 1] under the rules of
+ *                     kda_chunk_fwd_varlen (read on the device only, clamped
+ *                     into [0, T]; tokens outside every sequence keep what h
+ *                     held before)
+ *   T >= 0, D >= 1 (any width; rows of 16-byte multiples are the fast case).
+ * An empty sequence copies h0 to h_T. State and sums in fp32; decays over
+ * spans of tokens are exponentials of fp32 sums of log_alpha. Nothing depends
+ * on timing: equal inputs give equal bits.
+ */
+kda_status_t kda_recurrence_fwd(const void *log_alpha, const void *x, const float *h0, void *h, float *h_T,
+                                const int *cu_seqlens, int N, int T, int D, kda_dtype_t dtype, void *stream);
+
+/*
+ * Backward of kda_recurrence_fwd (the reverse recurrence): with c_T = d_h_T,
+ * for t = T .. 1
+ *
+ *     d_x_t = d_h_t + c_t,   c_{t-1} = exp(log_alpha_t) * d_x_t,
+ *     d_log_alpha_t = c_{t-1} * h_{t-1},   d_h0 = c_0.
+ *
+ *   log_alpha, h0, cu_seqlens, sizes: as in the forward pass
+ *   h               : the forward pass's output, dtype (the gradient of
+ *                     log_alpha takes h_{t-1} as it was rounded)
+ *   d_h             : [N, T, D] or packed [T, D], dtype
+ *   d_h_T           : [N, D] float; NULL means zero
+ *   d_x, d_log_alpha: like x, dtype, written (d_x may equal d_h)
+ *   d_h0            : [N, D] float, written; NULL: not computed
+ */
+kda_status_t kda_recurrence_bwd(const void *log_alpha, const void *h, const float *h0, const void *d_h,
+                                const float *d_h_T, void *d_x, void *d_log_alpha, float *d_h0,
+                                const int *cu_seqlens, int N, int T, int D, kda_dtype_t dtype, void *stream);
+
+/* One token per sequence: h_out = exp(log_alpha) * h_in + x, y = h_out rounded
+ * to dtype. log_alpha, x, y [N, D] dtype; h_in, h_out [N, D] float (h_out may
+ * equal h_in: the in-place update). */
+kda_status_t kda_recurrence_step(const void *log_alpha, const void *x, const float *h_in, float *h_out, void *y,
+                                 int N, int D, kda_dtype_t dtype, void *stream);
+
+/* The norm of a head's vector in kda_qk_norm_rope. */
+typedef enum {
+    KDA_NORM_L2 = 0, /* x / sqrt(sum x^2 + eps): the keys and queries of the delta rule */
+    KDA_NORM_RMS = 1 /* x / sqrt(mean x^2 + eps): the query/key norm of softmax layers  */
+} kda_norm_t;
+
+/*
+ * Queries and keys of a layer, normalised per head and rotated by position in
+ * one pass:
+ *
+ *     y = R(position) (w * x / sqrt(m + eps)),   q_out = q_scale * y(q), k_out = y(k)
+ *
+ * with m the sum or the mean of x^2 over the head, w an optional weight per
+ * channel, and R the rotation of channel pairs (i, i + rot/2) (interleaved =
+ * 0) or (2i, 2i + 1) (interleaved = 1) of the first rot channels by the angle
+ * whose cosine and sine stand in row `position`, column i of the tables; the
+ * other channels pass.
+ *
+ *   q               : [n, Hq, d] dtype, element (t, h, c) at
+ *                     t * q_stride_t + h * q_stride_h + c; k alike with Hk.
+ *                     Strides in elements, multiples of 16 bytes (slices of a
+ *                     fused projection are read in place)
+ *   q_weight, k_weight : [d] dtype, or NULL (ones)
+ *   cos, sin        : [max_pos, rot/2] float; ignored when positions is NULL
+ *   positions       : DEVICE [n] int32 (pos_bytes = 4) or int64 (8), or NULL: no
+ *                     rotation. Values are read on the device only and clamped
+ *                     into [0, max_pos)
+ *   q_out, k_out    : [n, Hq, d], [n, Hk, d] dtype, contiguous, written (each may
+ *                     equal its input where that is contiguous)
+ *   d               : multiple of 8 in [8, 256]; rot: multiple of 16 in [16, d]
+ *                     (with positions), Hq, Hk >= 0 (0: that side is absent)
+ *   eps             : > 0
+ * Arithmetic in fp32 (heads whose sum of squares leaves fp32 are rescaled),
+ * one rounding to dtype at the end.
+ */
+kda_status_t kda_qk_norm_rope(const void *q, const void *k, const void *q_weight, const void *k_weight,
+                              const float *cos, const float *sin, const void *positions, int pos_bytes, void *q_out,
+                              void *k_out, int n, int Hq, int Hk, int d, int rot, int max_pos, long long q_stride_t,
+                              long long q_stride_h, long long k_stride_t, long long k_stride_h, kda_norm_t norm,
+                              float eps, float q_scale, int interleaved, kda_dtype_t dtype, void *stream);
+
+/*
+ * Backward of kda_qk_norm_rope. d_q_out, d_k_out [n, H, d] dtype, contiguous;
+ * the inputs of the forward pass as there; d_q, d_k [n, H, d] dtype, contiguous,
+ * written. d_q_weight, d_k_weight [d] float, written: the sums over all tokens
+ * and heads, in a fixed order; NULL: not computed (the workspace is then not
+ * used and may be NULL).
+ *   workspace       : device scratch, 16-byte aligned, of
+ *                     kda_qk_norm_rope_bwd_workspace_size(...) bytes
+ */
+size_t kda_qk_norm_rope_bwd_workspace_size(int n, int Hq, int Hk, int d);
+kda_status_t kda_qk_norm_rope_bwd(const void *d_q_out, const void *d_k_out, const void *q, const void *k,
+                                  const void *q_weight, const void *k_weight, const float *cos, const float *sin,
+                                  const void *positions, int pos_bytes, void *d_q, void *d_k, float *d_q_weight,
+                                  float *d_k_weight, int n, int Hq, int Hk, int d, int rot, int max_pos,
+                                  long long q_stride_t, long long q_stride_h, long long k_stride_t,
+                                  long long k_stride_h, kda_norm_t norm, float eps, float q_scale, int interleaved,
+                                  kda_dtype_t dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Attention of one new token per sequence over a paged key-value cache (the
+ * softmax layer's counterpart of kda_decode_step): the token's key and value
+ * are put into the cache, and its query attends to the cache.
+ *
+ *     o = softmax(scale * q K^T) V     over the attended positions of sequence n
+ *
+ *   q               : [N, Hq, d] dtype; Hq a multiple of Hk: query head h reads
+ *                     key-value head h / (Hq / Hk)
+ *   k_new, v_new    : [N, Hk, d] dtype, or both NULL: nothing is put in
+ *   k_cache, v_cache: [n_pages, Hk, page_size, d] dtype, updated in place
+ *   page_table      : DEVICE int32 [N, max_pages]: position p of sequence n lies
+ *                     in page page_table[n][p / page_size], row p % page_size
+ *   seq_lens        : DEVICE int32 [N], positions held before the call. The new
+ *                     token gets position seq_lens[n]. A negative length marks a
+ *                     row of a padded batch: nothing is put in, o = 0
+ *   window          : > 0: only the last `window` positions, the new one among
+ *                     them, are attended; 0: all
+ *   o               : [N, Hq, d] dtype, written
+ *   lse             : [N, Hq] float, written: log of the sum of exp(score); NULL
+ *                     means not written
+ *   d               : 64 or 128
+ *   workspace       : device scratch, 16-byte aligned, of
+ *                     kda_attn_decode_workspace_size(...) bytes (0: may be NULL);
+ *                     two calls in flight at once must not share one
+ * page_table and seq_lens are read on the device only: positions past
+ * max_pages * page_size, and positions on pages outside [0, n_pages), are not
+ * attended, and a new token with such a position is not put in. A row without
+ * any attended position gives o = 0 and lse = -INFINITY. Rows of a page behind
+ * its sequence's last position are never read into a sum (they may hold NaN).
+ * The page that takes a new token must belong to its sequence alone.
+ * Scores, softmax statistics and sums in fp32; with KDA_BF16 the softmax
+ * weights are rounded to bf16 for the product with V. Equal inputs give equal
+ * bits.
+ */
+size_t kda_attn_decode_workspace_size(int N, int Hq, int Hk, int d);
+kda_status_t kda_attn_decode(const void *q, const void *k_new, const void *v_new, void *k_cache, void *v_cache,
+                             const int *page_table, const int *seq_lens, void *o, float *lse, int N, int Hq, int Hk,
+                             int d, int n_pages, int page_size, int max_pages, int window, float scale,
+                             kda_dtype_t dtype, void *workspace, size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }
