@@ -402,6 +402,9 @@ kda_status_t kda_attn_decode(const void* q, const void* k_new, const void* v_new
     if (d != 64 && d != 128) return KDA_ERR_UNSUPPORTED;
     // positions, and the work items of all rows, are counted in int32
     if ((long long)max_pages * page_size > 0x3fffffffLL || (long long)N * Hq > 0xffffffLL) return KDA_ERR_INVALID_ARG;
+    // so are the rows of a cache (one of more would not fit the device)
+    if ((long long)n_pages * page_size > 0x7fffffffLL || (long long)n_pages * page_size * Hk > 0x7fffffffLL)
+        return KDA_ERR_INVALID_ARG;
     if (N == 0) return KDA_OK;
     if (!good(q) || !good(o)) return KDA_ERR_INVALID_ARG;
     if ((k_new == nullptr) != (v_new == nullptr)) return KDA_ERR_INVALID_ARG;

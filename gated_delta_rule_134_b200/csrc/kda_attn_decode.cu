@@ -28,28 +28,47 @@ namespace kda {
 
 namespace {
 
-constexpr int kTile = 16;                          // positions of a tile
-constexpr int kHeads = 16;                         // query heads of a block (rows of the MMA)
-constexpr int kWarps = 4;                          // workers of a CTA
-constexpr int kCtas = 296;                         // two on each of 148 SMs
-constexpr int kWorkers = kCtas * kWarps;
+constexpr int kTile = 16;   // positions of a tile
+constexpr int kHeads = 16;  // query heads of a block
+constexpr int kWarps = 4;   // workers of a CTA
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// Stages of a worker's ring and CTAs of an SM: about 190 KB of cache rows in
+// flight an SM, by as many warps as the registers allow.
+template <typename T, int D> struct Plan;
+template <> struct Plan<__nv_bfloat16, 128> { static constexpr int kStages = 3, kCtasPerSm = 2; };
+template <> struct Plan<__nv_bfloat16, 64> { static constexpr int kStages = 4, kCtasPerSm = 3; };
+template <> struct Plan<float, 128> { static constexpr int kStages = 3, kCtasPerSm = 1; };
+template <> struct Plan<float, 64> { static constexpr int kStages = 3, kCtasPerSm = 2; };
+
+template <typename T, int D> struct Geometry : Plan<T, D> {
+    static constexpr int kRowBytes = D * (int)sizeof(T), kChunks = kRowBytes / 16;
+    static constexpr int kStageBytes = 2 * kTile * kRowBytes;  // K then V
+    static constexpr int kCtas = 148 * Plan<T, D>::kCtasPerSm, kWorkers = kCtas * kWarps;
+    static constexpr int kSmem = kWarps * Plan<T, D>::kStages * (kStageBytes + 16);
+};
+
+int workers_of(int bf16, int d) {
+    if (bf16) return d == 64 ? Geometry<__nv_bfloat16, 64>::kWorkers : Geometry<__nv_bfloat16, 128>::kWorkers;
+    return d == 64 ? Geometry<float, 64>::kWorkers : Geometry<float, 128>::kWorkers;
+}
 
 // The attended positions [first, last) of a row, and its number of tiles.
 struct Row {
     int held, first, last, tiles;
 };
 
-__device__ __forceinline__ Row row_of(const AttnDecodeArgs& a, int n) {
+__device__ __forceinline__ Row row_from(const AttnDecodeArgs& a, int held) {
     Row r;
-    r.held = a.seq_lens[n];
-    const bool put = a.k_new != nullptr && r.held >= 0;
-    const long long total = r.held < 0 ? 0 : (long long)r.held + (put ? 1 : 0);  // a length near 2^31 must not wrap
+    r.held = held;
+    const bool put = a.k_new != nullptr && held >= 0;
+    const long long total = held < 0 ? 0 : (long long)held + (put ? 1 : 0);  // a length near 2^31 must not wrap
     r.last = (int)min(total, (long long)a.max_pages * a.page_size);
     r.first = a.window ? (int)min(max(0ll, total - a.window), (long long)r.last) : 0;
     r.tiles = (r.last - r.first + kTile - 1) / kTile;
     return r;
 }
+__device__ __forceinline__ Row row_of(const AttnDecodeArgs& a, int n) { return row_from(a, a.seq_lens[n]); }
 
 // Workspace: per (worker, place) the pieces' O [heads][D], then their (m, l)
 // [heads], then per pair the worker that begins it and its number of pieces.
@@ -60,12 +79,12 @@ struct Pieces {
     int rows;
 };
 
-__host__ __device__ __forceinline__ Pieces pieces_of(void* ws, int G, int D) {
+__host__ __device__ __forceinline__ Pieces pieces_of(void* ws, int workers, int G, int D) {
     Pieces p;
     p.rows = G < kHeads ? G : kHeads;
     p.o = (float*)ws;
-    p.ml = (float2*)(p.o + (size_t)2 * kWorkers * p.rows * D);
-    p.pair = (int2*)(p.ml + (size_t)2 * kWorkers * p.rows);
+    p.ml = (float2*)(p.o + (size_t)2 * workers * p.rows * D);
+    p.pair = (int2*)(p.ml + (size_t)2 * workers * p.rows);
     return p;
 }
 
@@ -99,30 +118,179 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-template <int D> struct Bf16Stage {
-    static constexpr int kRowBytes = D * 2, kBytes = 2 * kTile * kRowBytes;  // K then V
-    static constexpr int kStages = 24576 / kBytes;                          // 24 KB a warp: 3 (D = 128) or 6
-};
-
-template <int D>
-constexpr int attn_smem_bytes() {
-    return kWarps * Bf16Stage<D>::kStages * (Bf16Stage<D>::kBytes + 16);
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 
-// HALF: at most 8 query heads, so rows 8..15 of the MMA are empty.
-template <int D, bool HALF>
-__global__ void __launch_bounds__(kWarps * 32, 2) attn_split_kernel(AttnDecodeArgs a) {
-    using St = Bf16Stage<D>;
-    using T = __nv_bfloat16;
-    constexpr int S = St::kStages, RB = St::kRowBytes, CH = RB / 16;  // 16-byte chunks of a row
-    extern __shared__ __align__(128) unsigned char smem[];
+// What the loading side tells the computing side about a stage's tile.
+struct Tile {
+    int out_row;    // n Hq + first query head of the block
+    int heads;      // of the block
+    unsigned bits;  // attended positions (0..15), kFresh, kEnds, place (2: a whole pair)
+};
+constexpr unsigned kFresh = 1u << 16, kEnds = 1u << 17;
+constexpr int kPlaceShift = 18;
+
+// The loading side of a worker: walks the tiles of its range and fills the ring.
+template <typename T, int D>
+struct Feed {
+    using Geo = Geometry<T, D>;
+    const AttnDecodeArgs& a;
+    int2* pair_out;
+    uint32_t ring;
+    int4* metas;
+    int worker, lane, G, blocks;
+    long long W;
+    // tile t of pair (hk, hb) of row n, `left` tiles to go
+    int n, hk, hb, t, left;
+    Row row;
+    int next_held;       // of row n + 1, loaded ahead
+    bool began, fresh;   // this worker holds the pair's first tile; the next tile begins a range of one pair
+    int page_at, off;    // lanes 0..15 (16..31 alike): the position's entry in the table, and its row in the page
+    int from, pages, pages2;  // lane i holds the table's entries from + i and from + 32 + i
+
+    __device__ __forceinline__ int entry(int i) const {
+        return i < a.max_pages ? a.page_table[(size_t)n * a.max_pages + i] : -1;
+    }
+    __device__ __forceinline__ void place_tile() {
+        const int pos = row.first + t * kTile + (lane & 15);
+        page_at = pos / a.page_size;
+        off = pos - page_at * a.page_size;
+    }
+    __device__ __forceinline__ void fetch_pages(bool anew) {
+        const int p0 = __shfl_sync(~0u, page_at, 0);
+        if (anew || p0 < from || p0 >= from + 64) {
+            from = p0 & ~31;
+            pages = entry(from + lane);
+            pages2 = entry(from + 32 + lane);
+        } else if (p0 >= from + 32) {
+            from += 32;
+            pages = pages2;
+            pages2 = entry(from + 32 + lane);
+        }
+    }
+    __device__ __forceinline__ void begin(int n_, long long rem, int count, bool any) {
+        left = count;
+        if (!any) return;
+        n = n_;
+        row = row_of(a, n);
+        next_held = n + 1 < a.N ? a.seq_lens[n + 1] : -1;
+        const int p = (int)(rem / row.tiles);
+        t = (int)(rem % row.tiles);
+        hk = p / blocks;
+        hb = p % blocks;
+        began = t == 0;
+        fresh = true;
+        place_tile();
+        fetch_pages(true);
+    }
+    __device__ __forceinline__ void advance() {
+        const bool pair_ends = t + 1 == row.tiles;
+        --left;
+        fresh = pair_ends;
+        if (left == 0) return;
+        if (!pair_ends) {
+            ++t;
+            if (a.page_size >= kTile) {
+                off += kTile;
+                if (off >= a.page_size) {
+                    off -= a.page_size;
+                    ++page_at;
+                }
+            } else {
+                place_tile();
+            }
+            fetch_pages(false);
+            return;
+        }
+        t = 0;
+        began = true;
+        bool anew = false;
+        if (++hb == blocks) {
+            hb = 0;
+            if (++hk == a.Hk) {
+                hk = 0;
+                anew = true;
+                do {  // tiles are left, so a row with some follows
+                    ++n;
+                    row = row_from(a, next_held);
+                    next_held = n + 1 < a.N ? a.seq_lens[n + 1] : -1;
+                } while (row.tiles == 0);
+            }
+        }
+        place_tile();
+        fetch_pages(anew);
+    }
+    // Copies the next tile into `stage` (nothing once the range is done); always commits one group.
+    __device__ __forceinline__ void issue(int stage) {
+        if (left > 0) {
+            constexpr int CH = Geo::kChunks, RB = Geo::kRowBytes, RowsAt = 32 / (CH < 32 ? CH : 32);
+            const int in = page_at - from;
+            const int lo = __shfl_sync(~0u, pages, in & 31), hi = __shfl_sync(~0u, pages2, in & 31);
+            const int page = in < 32 ? lo : hi, pos = row.first + t * kTile + (lane & 15);
+            const bool valid = pos < row.last && (unsigned)page < (unsigned)a.n_pages;
+            // row of the cache; the cache holds fewer than 2^31 of them
+            const int at = valid ? (page * a.Hk + hk) * a.page_size + off : -1;
+            const unsigned mask = __ballot_sync(~0u, valid) & 0xffffu;
+            const bool pair_ends = t + 1 == row.tiles, put = a.k_new && pair_ends && row.held < row.last;
+            const int new_row = put ? row.held - row.first - t * kTile : 0;  // the pair's last position
+            const int c = lane % CH, r0 = lane / CH;
+            const unsigned char *kb = (const unsigned char*)a.k_cache + c * 16, *vb = (const unsigned char*)a.v_cache + c * 16;
+            const uint32_t dst = ring + stage * Geo::kStageBytes + r0 * RB;
+            if (!(put && (mask >> new_row & 1))) {
+#pragma unroll
+                for (int i = 0; i < kTile / RowsAt; ++i) {
+                    const int r = i * RowsAt + r0, src = __shfl_sync(~0u, at, r);
+                    const size_t o = (size_t)(src < 0 ? 0 : src) * RB;
+                    const uint32_t to = dst + i * RowsAt * RB + ((c ^ (r & 7)) << 4);
+                    cp_async16(to, kb + o, src >= 0);
+                    cp_async16(to + kTile * RB, vb + o, src >= 0);
+                }
+            } else {
+                // The tile with the new token: its row comes from the arguments, and goes into the cache.
+                const size_t new_at = ((size_t)n * a.Hk + hk) * RB + c * 16;
+                const unsigned char *kn = (const unsigned char*)a.k_new + new_at, *vn = (const unsigned char*)a.v_new + new_at;
+#pragma unroll 1
+                for (int i = 0; i < kTile / RowsAt; ++i) {
+                    const int r = i * RowsAt + r0, src = __shfl_sync(~0u, at, r);
+                    const size_t o = (size_t)(src < 0 ? 0 : src) * RB;
+                    const uint32_t to = dst + i * RowsAt * RB + ((c ^ (r & 7)) << 4);
+                    const bool is_new = r == new_row;
+                    cp_async16(to, is_new ? kn : kb + o, src >= 0);
+                    cp_async16(to + kTile * RB, is_new ? vn : vb + o, src >= 0);
+                    if (is_new && hb == 0) {
+                        *reinterpret_cast<uint4*>((unsigned char*)a.k_cache + o + c * 16) = *reinterpret_cast<const uint4*>(kn);
+                        *reinterpret_cast<uint4*>((unsigned char*)a.v_cache + o + c * 16) = *reinterpret_cast<const uint4*>(vn);
+                    }
+                }
+            }
+            const bool range_ends = pair_ends || left == 1;
+            if (lane == 0) {
+                const int place = began ? (pair_ends ? 2 : 1) : 0;
+                const int head0 = hk * G + hb * kHeads;
+                metas[stage] = make_int4(n * a.Hq + head0, min(kHeads, G - hb * kHeads),
+                                         (int)(mask | (fresh ? kFresh : 0) | (range_ends ? kEnds : 0) | (unsigned)place << kPlaceShift), 0);
+                if (t == 0)
+                    pair_out[((size_t)n * a.Hk + hk) * blocks + hb] =
+                        make_int2(worker, row.tiles <= left ? 1 : 1 + (int)((row.tiles - left + W - 1) / W));
+            }
+            advance();
+        }
+        cp_async_commit();
+    }
+};
+
+// What the split kernels share before their loops: the range of this warp. False: it has none.
+// Rows without any attended position get their zeros here.
+template <typename T, int D>
+__device__ __forceinline__ bool find_range(const AttnDecodeArgs& a, const Pieces& ws, long long& W, int& count, int& row, long long& rem) {
+    constexpr int kWorkers = Geometry<T, D>::kWorkers, CH = Geometry<T, D>::kChunks;
     __shared__ long long s_part[kWarps], s_rem[kWarps];
     __shared__ int s_row[kWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int G = a.Hq / a.Hk, blocks = (G + kHeads - 1) / kHeads, P = a.Hk * blocks;
-    const Pieces ws = pieces_of(a.workspace, G, D);
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
+    const int G = a.Hq / a.Hk, P = a.Hk * ((G + kHeads - 1) / kHeads);
     // Tiles of all rows before thread tid's rows, and of all rows.
     const int per = (a.N + kWarps * 32 - 1) / (kWarps * 32), row0 = min(tid * per, a.N), row1 = min(row0 + per, a.N);
     long long mine = 0;
@@ -142,7 +310,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_split_kernel(AttnDecodeAr
         if (w < warp) before += s_part[w];
         total += s_part[w];
     }
-    const long long W = max(1ll, (total + kWorkers - 1) / kWorkers);  // tiles of a worker
+    W = total <= kWorkers ? 1 : (total + kWorkers - 1) / kWorkers;  // tiles of a worker
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
         long long u = (long long)(blockIdx.x * kWarps + w) * W;
@@ -154,7 +322,6 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_split_kernel(AttnDecodeAr
             s_rem[w] = u;
         }
     }
-    // rows without any attended position
     for (int n = blockIdx.x; n < a.N; n += gridDim.x) {
         if (row_of(a, n).tiles) continue;
         uint4* o = (uint4*)((T*)a.o + (size_t)n * a.Hq * D);
@@ -164,275 +331,274 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_split_kernel(AttnDecodeAr
         for (int i = tid; i < P; i += kWarps * 32) ws.pair[(size_t)n * P + i] = make_int2(0, 0);
     }
     __syncthreads();
+    const long long begin = (long long)(blockIdx.x * kWarps + warp) * W;
+    if (begin >= total) return false;
+    count = (int)min(W, total - begin);
+    row = s_row[warp];
+    rem = s_rem[warp];
+    return true;
+}
 
+// bf16: the positions are the rows of the MMAs, the query heads their columns
+// (NT blocks of 8), so that few heads waste little:
+//     S^T [16 x 8 NT] = K Q^T,  O^T [D x 8 NT] += V^T P^T.
+// The weights' maximum is a reference that moves only when a score passes it by
+// more than 2^8: until then weights reach 2^8, far from any overflow in 32
+// bits, and neither a reduction over the warp nor a rescaling is due.
+template <int D, int NT>
+__global__ void __launch_bounds__(kWarps * 32, Plan<__nv_bfloat16, D>::kCtasPerSm) attn_split_kernel(AttnDecodeArgs a) {
+    using T = __nv_bfloat16;
+    using Geo = Geometry<T, D>;
+    constexpr int S = Geo::kStages, RB = Geo::kRowBytes;
+    constexpr float kSlackLog2 = 8.f;
+    extern __shared__ __align__(128) unsigned char smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int G = a.Hq / a.Hk;
+    const Pieces ws = pieces_of(a.workspace, Geo::kWorkers, G, D);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    long long W, rem;
+    int count, row;
+    if (!find_range<T, D>(a, ws, W, count, row, rem)) return;
     const int worker = blockIdx.x * kWarps + warp;
-    if ((long long)worker * W >= total) return;
-    const int count = (int)min(W, total - (long long)worker * W);
-    unsigned char* ring = smem + (size_t)warp * S * St::kBytes;
-    int4* metas = reinterpret_cast<int4*>(smem + (size_t)kWarps * S * St::kBytes) + warp * S;
-    const uint32_t ring_u32 = sm100::smem_u32(ring);
+    const uint32_t ring = sm100::smem_u32(smem) + warp * S * Geo::kStageBytes;
+    int4* metas = reinterpret_cast<int4*>(smem + (size_t)kWarps * S * Geo::kStageBytes) + warp * S;
+    Feed<T, D> feed{a, ws.pair, ring, metas, worker, lane, G, (G + kHeads - 1) / kHeads, W};
+    feed.begin(row, rem, count, true);
+#pragma unroll 1
+    for (int s = 0; s < S - 1; ++s) feed.issue(s);
 
-    // ---- the loading side: tile t of pair p of row n, `left` tiles to go
-    int n = s_row[warp], left = count;
-    Row row = row_of(a, n);
-    int p = (int)(s_rem[warp] / row.tiles), t = (int)(s_rem[warp] % row.tiles);
-    bool began = t == 0;     // this worker holds the pair's first tile
-    bool fresh = true;       // the next tile begins a range of one pair
-    int page = -1;           // of position first + 16 t + lane (lanes 0..15)
-    auto look_up = [&]() {
-        const int pos = row.first + t * kTile + (lane & 15);
-        page = pos < row.last ? a.page_table[(size_t)n * a.max_pages + pos / a.page_size] : -1;
-    };
-    look_up();
-    auto issue = [&](int stage) {
-        if (left > 0) {
-            const int hk = p / blocks, hb = p % blocks;
-            const int pos = row.first + t * kTile + (lane & 15);
-            const bool valid = page >= 0 && page < a.n_pages;
-            const bool fresh_token = valid && a.k_new && pos == row.held;
-            const long long at = valid ? (((long long)page * a.Hk + hk) * a.page_size + pos % a.page_size) * D : -1;
-            const unsigned mask = __ballot_sync(~0u, valid && lane < 16), news = __ballot_sync(~0u, fresh_token && lane < 16);
-            const int new_row = news ? __ffs(news) - 1 : -1;
-            const uint32_t dst = ring_u32 + stage * St::kBytes;
-            const size_t new_at = ((size_t)n * a.Hk + hk) * D;
-            const int c = lane % CH;
-#pragma unroll
-            for (int i = 0; i < kTile * CH / 32; ++i) {
-                const int r = i * (32 / CH) + lane / CH;
-                const long long src = __shfl_sync(~0u, at, r);
-                const bool is_new = r == new_row, on = src >= 0;
-                const T* kp = is_new ? (const T*)a.k_new + new_at : (const T*)a.k_cache + (on ? src : 0);
-                const T* vp = is_new ? (const T*)a.v_new + new_at : (const T*)a.v_cache + (on ? src : 0);
-                const uint32_t to = dst + r * RB + ((c ^ (r & 7)) << 4);
-                cp_async16(to, kp + c * 8, on);
-                cp_async16(to + kTile * RB, vp + c * 8, on);
-            }
-            if (news && hb == 0) {  // put the new token's key and value where the table says
-                const long long to = __shfl_sync(~0u, at, new_row);
-                for (int i = lane; i < 2 * CH; i += 32) {
-                    const bool v = i >= CH;
-                    const int e = (v ? i - CH : i) * 8;
-                    *reinterpret_cast<uint4*>((T*)(v ? a.v_cache : a.k_cache) + to + e) =
-                        *reinterpret_cast<const uint4*>((const T*)(v ? a.v_new : a.k_new) + new_at + e);
-                }
-            }
-            const bool pair_ends = t + 1 == row.tiles, range_ends = pair_ends || left == 1;
-            if (lane == 0) {
-                const int place = began ? (pair_ends ? 2 : 1) : 0;  // 2: the whole pair
-                metas[stage] = make_int4(n, p, mask | (fresh ? 1u << 16 : 0) | (range_ends ? 1u << 17 : 0) | place << 18, 0);
-                if (t == 0)
-                    ws.pair[(size_t)n * P + p] =
-                        make_int2(worker, row.tiles <= left ? 1 : 1 + (int)((row.tiles - left + W - 1) / W));
-            }
-            --left;
-            fresh = range_ends;
-            if (!pair_ends) {
-                ++t;
-            } else if (left > 0) {
-                t = 0;
-                began = true;
-                if (++p == P) {
-                    p = 0;
-                    do row = row_of(a, ++n);
-                    while (row.tiles == 0);  // tiles are left, so a row with some follows
-                }
-            }
-            if (left > 0) look_up();
-        }
-        cp_async_commit();
-    };
-#pragma unroll
-    for (int s = 0; s < S - 1; ++s) issue(s);
-
-    // ---- the computing side
     const float scale2 = a.scale * kLog2e;
-    const int g = lane >> 2, c2 = (lane & 3) * 2;
-    uint32_t qf[D / 16][4];
-    float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    // ldmatrix rows of this lane: for K (positions x channels) and, transposed, for V
-    const int mat = lane >> 3, r8 = lane & 7;
-    const uint32_t k_row = (r8 + (mat >> 1) * 8) * RB, v_row = (r8 + (mat & 1) * 8) * RB;
+    const int g = lane >> 2, c2 = (lane & 3) * 2, mat = lane >> 3, r8 = lane & 7;
+    const uint32_t k_at = (r8 + (mat & 1) * 8) * RB, v_at = (r8 + (mat >> 1) * 8) * RB;
+    uint32_t qf[D / 16][NT][2];
+    float o[D / 16][NT][4], m[NT][2], l[NT][2];
     int stage = 0, into = S - 1;
+#pragma unroll 1
     for (int step = 0; step < count; ++step) {
         cp_async_wait<S - 2>();
         __syncwarp();
-        issue(into);
+        feed.issue(into);
         into = into + 1 == S ? 0 : into + 1;
         const int4 meta = metas[stage];
-        const uint32_t kt = ring_u32 + stage * St::kBytes, vt = kt + kTile * RB;
-        const int hk = meta.y / blocks, hb = meta.y % blocks, heads = min(kHeads, G - hb * kHeads);
-        const size_t out_row = (size_t)meta.x * a.Hq + (size_t)hk * G + hb * kHeads;  // of head 0
-        if (meta.z & (1 << 16)) {
-            const T* q = (const T*)a.q + out_row * D;
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-                const int at = ks * 16 + c2;
-                qf[ks][0] = g < heads ? *reinterpret_cast<const uint32_t*>(q + g * D + at) : 0u;
-                qf[ks][2] = g < heads ? *reinterpret_cast<const uint32_t*>(q + g * D + at + 8) : 0u;
-                qf[ks][1] = !HALF && g + 8 < heads ? *reinterpret_cast<const uint32_t*>(q + (g + 8) * D + at) : 0u;
-                qf[ks][3] = !HALF && g + 8 < heads ? *reinterpret_cast<const uint32_t*>(q + (g + 8) * D + at + 8) : 0u;
-            }
-#pragma unroll
-            for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-            m[0] = m[1] = -INFINITY;
-            l[0] = l[1] = 0.f;
-        }
-        float s[2][4] = {};
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-            uint32_t b[4];
-            ldsm4(b, kt + k_row + (((2 * ks + (mat & 1)) ^ r8) << 4));
-            mma_bf16(s[0], qf[ks], b[0], b[1]);
-            mma_bf16(s[1], qf[ks], b[2], b[3]);
-        }
-        // scores in log2 units; positions that are not attended: -infinity
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                s[j][e] = (meta.z >> (j * 8 + c2 + (e & 1))) & 1 ? s[j][e] * scale2 : -INFINITY;
-        float keep[2] = {1.f, 1.f};
-#pragma unroll
-        for (int h = 0; h < (HALF ? 1 : 2); ++h) {
-            float top = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
-            top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-            top = fmaxf(fmaxf(top, __shfl_xor_sync(~0u, top, 2)), m[h]);
-            const float base = top == -INFINITY ? 0.f : top;  // nothing attended so far: weights of 0
-            keep[h] = exp2_fast(m[h] - base);
-            m[h] = top;
-            float sum = 0.f;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                s[j][2 * h] = exp2_fast(s[j][2 * h] - base);
-                s[j][2 * h + 1] = exp2_fast(s[j][2 * h + 1] - base);
-                sum += s[j][2 * h] + s[j][2 * h + 1];
-            }
-            l[h] = fmaf(l[h], keep[h], sum);
-        }
-        if (__any_sync(~0u, keep[0] != 1.f || keep[1] != 1.f)) {
-#pragma unroll
-            for (int j = 0; j < D / 8; ++j) {
-                o[j][0] *= keep[0];
-                o[j][1] *= keep[0];
-                if (!HALF) {
-                    o[j][2] *= keep[1];
-                    o[j][3] *= keep[1];
-                }
-            }
-        }
-        // the weights as the left operand (bf16, at most half a step off each; l sums them unrounded)
-        const uint32_t pf[4] = {pack_bf16(s[0][0], s[0][1]), HALF ? 0u : pack_bf16(s[0][2], s[0][3]),
-                                pack_bf16(s[1][0], s[1][1]), HALF ? 0u : pack_bf16(s[1][2], s[1][3])};
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-            uint32_t b[4];
-            ldsm4_trans(b, vt + v_row + (((2 * j + (mat >> 1)) ^ r8) << 4));
-            mma_bf16(o[2 * j], pf, b[0], b[1]);
-            mma_bf16(o[2 * j + 1], pf, b[2], b[3]);
-        }
-        if (meta.z & (1 << 17)) {
-            const int place = meta.z >> 18;
-#pragma unroll
-            for (int h = 0; h < (HALF ? 1 : 2); ++h) {
-                float sum = l[h];
-                sum += __shfl_xor_sync(~0u, sum, 1);
-                sum += __shfl_xor_sync(~0u, sum, 2);
-                const int head = g + 8 * h;
-                if (head >= heads) continue;
-                if (place == 2) {
-                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                    uint32_t* to = reinterpret_cast<uint32_t*>((T*)a.o + (out_row + head) * D + c2);
-#pragma unroll
-                    for (int j = 0; j < D / 8; ++j) to[j * 4] = pack_bf16(o[j][2 * h] * inv, o[j][2 * h + 1] * inv);
-                    if (a.lse && (lane & 3) == 0)
-                        a.lse[out_row + head] = sum == 0.f ? -INFINITY : fmaf(m[h], kLn2, logf(sum));
-                } else {
-                    const size_t at = (size_t)(2 * worker + place) * ws.rows + head;
-                    float* to = ws.o + at * D + c2;
-#pragma unroll
-                    for (int j = 0; j < D / 8; ++j)
-                        *reinterpret_cast<float2*>(to + j * 8) = make_float2(o[j][2 * h], o[j][2 * h + 1]);
-                    if ((lane & 3) == 0) ws.ml[at] = make_float2(m[h], sum);
-                }
-            }
-        }
+        const unsigned bits = (unsigned)meta.z;
+        const int heads = meta.y;
+        const uint32_t kt = ring + stage * Geo::kStageBytes, vt = kt + kTile * RB;
         stage = stage + 1 == S ? 0 : stage + 1;
+        if (bits & kFresh) {
+            const T* q = (const T*)a.q + (size_t)meta.x * D + c2;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const bool on = g + 8 * j < heads;
+                const T* qh = q + (on ? g + 8 * j : 0) * D;
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    qf[ks][j][0] = on ? *reinterpret_cast<const uint32_t*>(qh + ks * 16) : 0u;
+                    qf[ks][j][1] = on ? *reinterpret_cast<const uint32_t*>(qh + ks * 16 + 8) : 0u;
+                }
+                m[j][0] = m[j][1] = -INFINITY;
+                l[j][0] = l[j][1] = 0.f;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) o[i][j][0] = o[i][j][1] = o[i][j][2] = o[i][j][3] = 0.f;
+            }
+        }
+        float s[NT][4] = {}, s2[NT][4] = {};  // two sums: half the chain of dependent products
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ks += 2) {
+            uint32_t kf[2][4];
+            ldsm4(kf[0], kt + k_at + (((2 * ks + (mat >> 1)) ^ r8) << 4));
+            ldsm4(kf[1], kt + k_at + (((2 * ks + 2 + (mat >> 1)) ^ r8) << 4));
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                mma_bf16(s[j], kf[0], qf[ks][j][0], qf[ks][j][1]);
+                mma_bf16(s2[j], kf[1], qf[ks + 1][j][0], qf[ks + 1][j][1]);
+            }
+        }
+        // scores in log2 units: elements 0, 1 are position g of heads c2, c2 + 1 (+ 8 j), elements 2, 3 position g + 8
+        const bool on_lo = bits >> g & 1, on_hi = bits >> (g + 8) & 1;
+        bool past = false;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                s[j][e] = on_lo ? (s[j][e] + s2[j][e]) * scale2 : -INFINITY;
+                s[j][e + 2] = on_hi ? (s[j][e + 2] + s2[j][e + 2]) * scale2 : -INFINITY;
+                past |= fmaxf(s[j][e], s[j][e + 2]) > m[j][e] + kSlackLog2;
+            }
+        if (__any_sync(~0u, past)) {  // move the references to the maxima, for all heads of the warp
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float top = fmaxf(s[j][e], s[j][e + 2]);
+#pragma unroll
+                    for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, x));
+                    top = fmaxf(top, m[j][e]);
+                    const float keep = m[j][e] == top ? 1.f : exp2_fast(m[j][e] - top);
+                    m[j][e] = top;
+                    l[j][e] *= keep;
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+                        o[i][j][e] *= keep;
+                        o[i][j][e + 2] *= keep;
+                    }
+                }
+        }
+        uint32_t pf[NT][2];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float base = m[j][e] == -INFINITY ? 0.f : m[j][e];  // nothing attended so far: weights of 0
+                s[j][e] = exp2_fast(s[j][e] - base);
+                s[j][e + 2] = exp2_fast(s[j][e + 2] - base);
+                l[j][e] += s[j][e] + s[j][e + 2];
+            }
+            // the weights as the right operand (bf16, at most half a step off each; l sums them unrounded)
+            pf[j][0] = transpose8x8(pack_bf16(s[j][0], s[j][1]));
+            pf[j][1] = transpose8x8(pack_bf16(s[j][2], s[j][3]));
+        }
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+            uint32_t vf[4];
+            ldsm4_trans(vf, vt + v_at + (((2 * i + (mat & 1)) ^ r8) << 4));
+#pragma unroll
+            for (int j = 0; j < NT; ++j) mma_bf16(o[i][j], vf, pf[j][0], pf[j][1]);
+        }
+        if (bits & kEnds) {
+            const int place = (int)(bits >> kPlaceShift);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                float sum[2], inv[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    sum[e] = l[j][e];
+#pragma unroll
+                    for (int x = 4; x < 32; x <<= 1) sum[e] += __shfl_xor_sync(~0u, sum[e], x);
+                    inv[e] = sum[e] == 0.f ? 0.f : 1.f / sum[e];
+                }
+                const int head = c2 + 8 * j;  // of element 0; element 1: the next
+                if (place == 2) {
+                    T* to = (T*)a.o + (size_t)(meta.x + g + 8 * j) * D + c2;
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {  // transposed: lane 4 h + x holds channels 2 x, 2 x + 1 of head h
+                        const uint32_t lo = transpose8x8(pack_bf16(o[i][j][0] * inv[0], o[i][j][1] * inv[1]));
+                        const uint32_t hi = transpose8x8(pack_bf16(o[i][j][2] * inv[0], o[i][j][3] * inv[1]));
+                        if (g + 8 * j < heads) {
+                            *reinterpret_cast<uint32_t*>(to + i * 16) = lo;
+                            *reinterpret_cast<uint32_t*>(to + i * 16 + 8) = hi;
+                        }
+                    }
+                    if (a.lse && g < 2 && head + g < heads) {
+                        const float all = g ? sum[1] : sum[0], ref = g ? m[j][1] : m[j][0];
+                        a.lse[meta.x + head + g] = all == 0.f ? -INFINITY : fmaf(ref, kLn2, logf(all));
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        if (head + e >= heads) continue;
+                        const size_t at = (size_t)(2 * worker + place) * ws.rows + head + e;
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i) {
+                            ws.o[at * D + i * 16 + g] = o[i][j][e];
+                            ws.o[at * D + i * 16 + 8 + g] = o[i][j][e + 2];
+                        }
+                        if (g == 0) ws.ml[at] = make_float2(m[j][e], sum[e]);
+                    }
+                }
+            }
+        }
     }
     cp_async_wait<0>();
 }
 
-// Joins the pieces of every pair that lies in several workers, in their order:
-// piece 0 in place 1 of the worker that begins the pair, the others in place 0
-// of the workers after it. blockIdx.x: a run of `chunk` pairs; blockIdx.y: heads.
+// Joins the pieces of every (pair, query head) that lies in several workers, in
+// their order: piece 0 in place 1 of the worker that begins the pair, the others
+// in place 0 of the workers after it. WARPS warps share the pieces: 8 where
+// there are few pairs, so many pieces of each, 1 where there are many. A warp
+// loads up to four pieces at once, maxima and sums with them, so that the chain
+// of dependent loads is two long.
 constexpr int kJoinWarps = 8;
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(AttnDecodeArgs a, int pairs, int chunk) {
-    constexpr int E = D / 32;
-    __shared__ float so[kJoinWarps][D], sl[kJoinWarps];
+template <typename T, int D, int WARPS>
+__global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(AttnDecodeArgs a, int items) {
+    constexpr int E = D / 32, B = 4;
+    __shared__ float so[WARPS == 1 ? 1 : WARPS][D];
+    __shared__ float2 sml[WARPS];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = a.Hq / a.Hk, blocks = (G + kHeads - 1) / kHeads, P = a.Hk * blocks;
-    const Pieces ws = pieces_of(a.workspace, G, D);
+    const Pieces ws = pieces_of(a.workspace, Geometry<T, D>::kWorkers, G, D);
+    const int item = WARPS == 1 ? blockIdx.x * kJoinWarps + warp : blockIdx.x;
+    if (item >= items) return;
+    const int i = item / ws.rows, h = item % ws.rows;
+    const int n = i / P, p = i % P, hk = p / blocks, hb = p % blocks;
+    if (h >= G - hb * kHeads) return;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    __shared__ int2 found[kJoinWarps * 32];
-    const int begin = blockIdx.x * chunk, end = min(begin + chunk, pairs);
-    for (int i = begin, from = begin; i < end; ++i) {
-        if (i == from) {  // the next 256 pairs; most of them lie in one worker
-            const int2 mine = i + (int)threadIdx.x < end ? ws.pair[i + threadIdx.x] : make_int2(0, 0);
-            found[threadIdx.x] = mine;
-            from += kJoinWarps * 32;
-            const bool some = __syncthreads_or(mine.y > 1);
-            if (!some) {
-                i = from - 1;
-                continue;
+    const int2 pair = ws.pair[i];
+    if (pair.y < 2) return;
+    auto slot = [&](int k) { return (size_t)(2 * (pair.x + k) + (k == 0 ? 1 : 0)) * ws.rows + h; };
+    float acc[E] = {}, sum = 0.f, ref = -INFINITY;
+    for (int k = WARPS == 1 ? 0 : warp; k < pair.y; k += WARPS * B) {
+        float2 ml[B];
+        float x[B][E];
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            const bool on = k + b * WARPS < pair.y;
+            const size_t at = slot(on ? k + b * WARPS : k);
+            ml[b] = on ? ws.ml[at] : make_float2(-INFINITY, 0.f);
+            const float* from = ws.o + at * D + lane * E;
+            if constexpr (E == 4) {
+                const float4 v = *reinterpret_cast<const float4*>(from);
+                x[b][0] = v.x; x[b][1] = v.y; x[b][2] = v.z; x[b][3] = v.w;
+            } else {
+                const float2 v = *reinterpret_cast<const float2*>(from);
+                x[b][0] = v.x; x[b][1] = v.y;
             }
         }
-        const int2 pair = found[(i - begin) % (kJoinWarps * 32)];
-        if (i + 1 == from) __syncthreads();  // all have read it before the next 256 replace it
-        if (pair.y < 2) continue;
-        const int n = i / P, p = i % P, hk = p / blocks, hb = p % blocks, heads = min(kHeads, G - hb * kHeads);
-        for (int h = blockIdx.y; h < heads; h += gridDim.y) {
-            auto slot = [&](int k) { return (size_t)(2 * (pair.x + k) + (k == 0 ? 1 : 0)) * ws.rows + h; };
-            float top = -INFINITY;
-            for (int k = lane; k < pair.y; k += 32) top = fmaxf(top, ws.ml[slot(k)].x);
+        float top = ref;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-            const float base = top == -INFINITY ? 0.f : top;
-            float acc[E] = {}, l = 0.f;
-#pragma unroll 4
-            for (int k = warp; k < pair.y; k += kJoinWarps) {
-                const size_t at = slot(k);
-                const float2 ml = ws.ml[at];
-                const float f = exp2_fast(ml.x - base);
-                l = fmaf(ml.y, f, l);
-                const float* from = ws.o + at * D + lane * E;
-                if constexpr (E == 4) {
-                    const float4 x = *reinterpret_cast<const float4*>(from);
-                    acc[0] = fmaf(x.x, f, acc[0]); acc[1] = fmaf(x.y, f, acc[1]);
-                    acc[2] = fmaf(x.z, f, acc[2]); acc[3] = fmaf(x.w, f, acc[3]);
-                } else {
-                    const float2 x = *reinterpret_cast<const float2*>(from);
-                    acc[0] = fmaf(x.x, f, acc[0]); acc[1] = fmaf(x.y, f, acc[1]);
-                }
-            }
+        for (int b = 0; b < B; ++b) top = fmaxf(top, ml[b].x);
+        const float keep = ref == top ? 1.f : exp2_fast(ref - top);
+        ref = top;
+        sum *= keep;
 #pragma unroll
-            for (int e = 0; e < E; ++e) so[warp][lane * E + e] = acc[e];
-            if (lane == 0) sl[warp] = l;
-            __syncthreads();
-            float sum = 0.f;
+        for (int e = 0; e < E; ++e) acc[e] *= keep;
 #pragma unroll
-            for (int w = 0; w < kJoinWarps; ++w) sum += sl[w];
-            const size_t out = (size_t)n * a.Hq + (size_t)hk * G + hb * kHeads + h;
-            for (int c = threadIdx.x; c < D; c += kJoinWarps * 32) {
-                float x = 0.f;
+        for (int b = 0; b < B; ++b) {
+            if (ml[b].x == -INFINITY) continue;  // nothing attended in this piece
+            const float f = exp2_fast(ml[b].x - top);
+            sum = fmaf(ml[b].y, f, sum);
 #pragma unroll
-                for (int w = 0; w < kJoinWarps; ++w) x += so[w][c];
-                ((T*)a.o)[out * D + c] = from_f32<T>(sum == 0.f ? 0.f : x / sum);
-            }
-            if (a.lse && threadIdx.x == 0) a.lse[out] = sum == 0.f ? -INFINITY : fmaf(top, kLn2, logf(sum));
-            __syncthreads();
+            for (int e = 0; e < E; ++e) acc[e] = fmaf(x[b][e], f, acc[e]);
         }
     }
+    const size_t out = (size_t)n * a.Hq + (size_t)hk * G + hb * kHeads + h;
+    if constexpr (WARPS == 1) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) ((T*)a.o)[out * D + lane * E + e] = from_f32<T>(sum == 0.f ? 0.f : acc[e] / sum);
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) so[warp][lane * E + e] = acc[e];
+        if (lane == 0) sml[warp] = make_float2(ref, sum);
+        __syncthreads();
+        ref = -INFINITY;
+        sum = 0.f;
+        float f[WARPS];
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) ref = fmaxf(ref, sml[w].x);
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+            f[w] = sml[w].x == -INFINITY ? 0.f : exp2_fast(sml[w].x - ref);
+            sum = fmaf(sml[w].y, f[w], sum);
+        }
+        for (int c = threadIdx.x; c < D; c += WARPS * 32) {
+            float x = 0.f;
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) x = fmaf(so[w][c], f[w], x);
+            ((T*)a.o)[out * D + c] = from_f32<T>(sum == 0.f ? 0.f : x / sum);
+        }
+    }
+    if (a.lse && (WARPS == 1 ? lane : (int)threadIdx.x) == 0)
+        a.lse[out] = sum == 0.f ? -INFINITY : fmaf(ref, kLn2, logf(sum));
 }
 
 template <typename T, int D>
@@ -501,23 +667,24 @@ __global__ void attn_decode_kernel(AttnDecodeArgs a) {
 
 size_t attn_decode_workspace_bytes(int N, int Hq, int Hk, int d) {
     const int G = Hq / Hk, blocks = (G + kHeads - 1) / kHeads;
-    const Pieces p = pieces_of(nullptr, G, d);
+    const int bf = workers_of(1, d), f = workers_of(0, d);
+    const Pieces p = pieces_of(nullptr, bf > f ? bf : f, G, d);
     return (size_t)((char*)(p.pair + (size_t)N * Hk * blocks) - (char*)nullptr);
 }
 
-template <int D>
-static cudaError_t launch_attn_bf16(const AttnDecodeArgs& a, cudaStream_t stream) {
+template <typename T, int D, typename Kernel>
+static cudaError_t launch_attn(Kernel split, const AttnDecodeArgs& a, cudaStream_t stream) {
+    using Geo = Geometry<T, D>;
     const int G = a.Hq / a.Hk, pairs = a.N * a.Hk * ((G + kHeads - 1) / kHeads);
-    auto split = G <= 8 ? attn_split_kernel<D, true> : attn_split_kernel<D, false>;
-    constexpr int smem = attn_smem_bytes<D>();
-    cudaError_t err = cudaFuncSetAttribute(split, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t err = cudaFuncSetAttribute(split, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo::kSmem);
     if (err != cudaSuccess) return err;
-    split<<<kCtas, kWarps * 32, smem, stream>>>(a);
+    split<<<Geo::kCtas, kWarps * 32, Geo::kSmem, stream>>>(a);
     if ((err = cudaGetLastError()) != cudaSuccess) return err;
-    // The join starts while the split kernel runs (programmatic dependent launch) and waits for its end there.
-    const int chunk = (pairs + kWorkers - 1) / kWorkers;
+    // The join is launched while the split kernel runs (programmatic dependent launch) and waits for its end.
+    const bool few = pairs < 148;
+    const int items = pairs * (G < kHeads ? G : kHeads);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((pairs + chunk - 1) / chunk, pairs < 148 ? (G < kHeads ? G : kHeads) : 1);
+    cfg.gridDim = dim3(few ? items : (items + kJoinWarps - 1) / kJoinWarps);
     cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = stream;
     cudaLaunchAttribute attr;
@@ -525,7 +692,13 @@ static cudaError_t launch_attn_bf16(const AttnDecodeArgs& a, cudaStream_t stream
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_join_kernel<__nv_bfloat16, D>, a, pairs, chunk);
+    return cudaLaunchKernelEx(&cfg, few ? attn_join_kernel<T, D, kJoinWarps> : attn_join_kernel<T, D, 1>, a, items);
+}
+
+template <int D>
+static cudaError_t launch_attn_bf16(const AttnDecodeArgs& a, cudaStream_t stream) {
+    if (a.Hq / a.Hk <= 8) return launch_attn<__nv_bfloat16, D>(attn_split_kernel<D, 1>, a, stream);
+    return launch_attn<__nv_bfloat16, D>(attn_split_kernel<D, 2>, a, stream);
 }
 
 cudaError_t launch_attn_decode(const AttnDecodeArgs& a, cudaStream_t stream) {
