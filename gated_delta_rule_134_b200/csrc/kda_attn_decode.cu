@@ -13,7 +13,9 @@
 // Split: the positions of all (sequence, key-value head, block of 16 query
 // heads) are cut into tiles of 16, and the list of all tiles is cut into equal
 // contiguous ranges, one per warp ("worker"), whatever the lengths are: a
-// batch of one long and many short contexts loads every SM alike. Workers find
+// batch of one long and many short contexts loads every SM alike. (To begin and
+// to end a pair costs as much as some tiles, so each pair counts kBegin more.)
+// Workers find
 // their range from seq_lens on the device. A worker that holds all tiles of a
 // pair writes its output; else it leaves (m, l, O) in the workspace, where it
 // has two places: 0 for a range that continues a pair, 1 for one that begins a
@@ -31,6 +33,7 @@ namespace {
 constexpr int kTile = 16;   // positions of a tile
 constexpr int kHeads = 16;  // query heads of a block
 constexpr int kWarps = 4;   // workers of a CTA
+constexpr int kBegin = 3;   // what a pair costs beside its tiles, in tiles
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // Stages of a worker's ring and CTAs of an SM: about 190 KB of cache rows in
@@ -69,6 +72,8 @@ __device__ __forceinline__ Row row_from(const AttnDecodeArgs& a, int held) {
     return r;
 }
 __device__ __forceinline__ Row row_of(const AttnDecodeArgs& a, int n) { return row_from(a, a.seq_lens[n]); }
+// A pair of this row in the list of all work: kBegin units, then its tiles.
+__device__ __forceinline__ int units_of(const Row& r) { return r.tiles ? r.tiles + kBegin : 0; }
 
 // Workspace: per (worker, place) the pieces' O [heads][D], then their (m, l)
 // [heads], then per pair the worker that begins it and its number of pieces.
@@ -143,8 +148,8 @@ struct Feed {
     int4* metas;
     int worker, lane, G, blocks;
     long long W;
-    // tile t of pair (hk, hb) of row n, `left` tiles to go
-    int n, hk, hb, t, left;
+    // tile t of pair (hk, hb) of row n, `left` units to go (0: the range is done)
+    int n, hk, hb, t, left, issued;
     Row row;
     int next_held;       // of row n + 1, loaded ahead
     bool began, fresh;   // this worker holds the pair's first tile; the next tile begins a range of one pair
@@ -171,14 +176,16 @@ struct Feed {
             pages2 = entry(from + 32 + lane);
         }
     }
-    __device__ __forceinline__ void begin(int n_, long long rem, int count, bool any) {
+    // `count` units from unit `rem` of row n_
+    __device__ __forceinline__ void begin(int n_, long long rem, int count) {
         left = count;
-        if (!any) return;
+        issued = 0;
         n = n_;
         row = row_of(a, n);
         next_held = n + 1 < a.N ? a.seq_lens[n + 1] : -1;
-        const int p = (int)(rem / row.tiles);
-        t = (int)(rem % row.tiles);
+        const int p = (int)(rem / units_of(row)), v = (int)(rem % units_of(row)) - kBegin;
+        t = max(v, 0);
+        left = max(left + min(v, 0), 0);
         hk = p / blocks;
         hb = p % blocks;
         began = t == 0;
@@ -205,6 +212,7 @@ struct Feed {
             fetch_pages(false);
             return;
         }
+        if ((left = max(left - kBegin, 0)) == 0) return;
         t = 0;
         began = true;
         bool anew = false;
@@ -267,6 +275,12 @@ struct Feed {
                 }
             }
             const bool range_ends = pair_ends || left == 1;
+            if (fresh) {  // the queries are read when the tile is worked on: have them in L2 by then
+                const int head0 = hk * G + hb * kHeads, lines = min(kHeads, G - hb * kHeads) * RB / 128;
+                if (lane < lines)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"((const char*)a.q + ((size_t)n * a.Hq + head0) * RB + lane * 128));
+            }
+            ++issued;
             if (lane == 0) {
                 const int place = began ? (pair_ends ? 2 : 1) : 0;
                 const int head0 = hk * G + hb * kHeads;
@@ -291,10 +305,10 @@ __device__ __forceinline__ bool find_range(const AttnDecodeArgs& a, const Pieces
     __shared__ int s_row[kWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = a.Hq / a.Hk, P = a.Hk * ((G + kHeads - 1) / kHeads);
-    // Tiles of all rows before thread tid's rows, and of all rows.
+    // Units of all rows before thread tid's rows, and of all rows.
     const int per = (a.N + kWarps * 32 - 1) / (kWarps * 32), row0 = min(tid * per, a.N), row1 = min(row0 + per, a.N);
     long long mine = 0;
-    for (int n = row0; n < row1; ++n) mine += row_of(a, n).tiles;
+    for (int n = row0; n < row1; ++n) mine += units_of(row_of(a, n));
     mine *= P;
     long long incl = mine;
 #pragma unroll
@@ -310,14 +324,14 @@ __device__ __forceinline__ bool find_range(const AttnDecodeArgs& a, const Pieces
         if (w < warp) before += s_part[w];
         total += s_part[w];
     }
-    W = total <= kWorkers ? 1 : (total + kWorkers - 1) / kWorkers;  // tiles of a worker
+    W = total <= kWorkers ? 1 : (total + kWorkers - 1) / kWorkers;  // units of a worker
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
         long long u = (long long)(blockIdx.x * kWarps + w) * W;
         if (u >= before && u < before + mine) {
             u -= before;
             int n = row0;
-            for (long long tiles; u >= (tiles = (long long)row_of(a, n).tiles * P); ++n) u -= tiles;
+            for (long long units; u >= (units = (long long)units_of(row_of(a, n)) * P); ++n) u -= units;
             s_row[w] = n;
             s_rem[w] = u;
         }
@@ -363,7 +377,7 @@ __global__ void __launch_bounds__(kWarps * 32, Plan<__nv_bfloat16, D>::kCtasPerS
     const uint32_t ring = sm100::smem_u32(smem) + warp * S * Geo::kStageBytes;
     int4* metas = reinterpret_cast<int4*>(smem + (size_t)kWarps * S * Geo::kStageBytes) + warp * S;
     Feed<T, D> feed{a, ws.pair, ring, metas, worker, lane, G, (G + kHeads - 1) / kHeads, W};
-    feed.begin(row, rem, count, true);
+    feed.begin(row, rem, count);
 #pragma unroll 1
     for (int s = 0; s < S - 1; ++s) feed.issue(s);
 
@@ -374,7 +388,7 @@ __global__ void __launch_bounds__(kWarps * 32, Plan<__nv_bfloat16, D>::kCtasPerS
     float o[D / 16][NT][4], m[NT][2], l[NT][2];
     int stage = 0, into = S - 1;
 #pragma unroll 1
-    for (int step = 0; step < count; ++step) {
+    for (int step = 0; step < feed.issued; ++step) {
         cp_async_wait<S - 2>();
         __syncwarp();
         feed.issue(into);
