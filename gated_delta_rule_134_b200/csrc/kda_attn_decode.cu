@@ -129,6 +129,25 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     return y;
 }
 
+__device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// x = hi + lo + at most 2^-22 |x|, each part a tf32 number. An infinity goes into
+// lo alone: products with the other operand's hi then have its sign, and there
+// is no infinity times a part that happens to be zero.
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
+    if (!(fabsf(x) < INFINITY)) hi = 0u;
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(x - __uint_as_float(hi)));
+}
+__device__ __forceinline__ float lds_f32(uint32_t at) {
+    float x;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(at) : "memory");
+    return x;
+}
+
 // What the loading side tells the computing side about a stage's tile.
 struct Tile {
     int out_row;    // n Hq + first query head of the block
@@ -353,17 +372,23 @@ __device__ __forceinline__ bool find_range(const AttnDecodeArgs& a, const Pieces
     return true;
 }
 
-// bf16: the positions are the rows of the MMAs, the query heads their columns
-// (NT blocks of 8), so that few heads waste little:
+// The positions are the rows of the MMAs, the query heads their columns (NT
+// blocks of 8), so that few heads waste little:
 //     S^T [16 x 8 NT] = K Q^T,  O^T [D x 8 NT] += V^T P^T.
+// bf16 operands go in as they are, the weights rounded to bf16. 32-bit operands
+// are split into two tf32 parts each, and three products taken (the fourth,
+// lo * lo, is below 2^-22 of the whole), which keeps 32-bit accuracy at a quarter
+// of the instructions that multiply-adds would take.
 // The weights' maximum is a reference that moves only when a score passes it by
 // more than 2^8: until then weights reach 2^8, far from any overflow in 32
 // bits, and neither a reduction over the warp nor a rescaling is due.
-template <int D, int NT>
-__global__ void __launch_bounds__(kWarps * 32, Plan<__nv_bfloat16, D>::kCtasPerSm) attn_split_kernel(AttnDecodeArgs a) {
-    using T = __nv_bfloat16;
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kWarps * 32, Plan<T, D>::kCtasPerSm) attn_split_kernel(AttnDecodeArgs a) {
     using Geo = Geometry<T, D>;
+    constexpr bool BF = sizeof(T) == 2;
     constexpr int S = Geo::kStages, RB = Geo::kRowBytes;
+    constexpr int KS = BF ? D / 16 : D / 8;  // steps of the K Q^T product
+    constexpr bool SPLIT_Q = !BF && NT == 1;  // both tf32 parts of the queries kept (16 heads: split anew each time)
     constexpr float kSlackLog2 = 8.f;
     extern __shared__ __align__(128) unsigned char smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -382,9 +407,9 @@ __global__ void __launch_bounds__(kWarps * 32, Plan<__nv_bfloat16, D>::kCtasPerS
     for (int s = 0; s < S - 1; ++s) feed.issue(s);
 
     const float scale2 = a.scale * kLog2e;
-    const int g = lane >> 2, c2 = (lane & 3) * 2, mat = lane >> 3, r8 = lane & 7;
+    const int g = lane >> 2, c = lane & 3, c2 = c * 2, mat = lane >> 3, r8 = lane & 7;
     const uint32_t k_at = (r8 + (mat & 1) * 8) * RB, v_at = (r8 + (mat >> 1) * 8) * RB;
-    uint32_t qf[D / 16][NT][2];
+    uint32_t qf[KS][NT][2], ql[SPLIT_Q ? KS : 1][NT][2];
     float o[D / 16][NT][4], m[NT][2], l[NT][2];
     int stage = 0, into = S - 1;
 #pragma unroll 1
@@ -399,15 +424,23 @@ __global__ void __launch_bounds__(kWarps * 32, Plan<__nv_bfloat16, D>::kCtasPerS
         const uint32_t kt = ring + stage * Geo::kStageBytes, vt = kt + kTile * RB;
         stage = stage + 1 == S ? 0 : stage + 1;
         if (bits & kFresh) {
-            const T* q = (const T*)a.q + (size_t)meta.x * D + c2;
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
                 const bool on = g + 8 * j < heads;
-                const T* qh = q + (on ? g + 8 * j : 0) * D;
+                const T* qh = (const T*)a.q + (size_t)(meta.x + (on ? g + 8 * j : 0)) * D;
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    qf[ks][j][0] = on ? *reinterpret_cast<const uint32_t*>(qh + ks * 16) : 0u;
-                    qf[ks][j][1] = on ? *reinterpret_cast<const uint32_t*>(qh + ks * 16 + 8) : 0u;
+                for (int ks = 0; ks < KS; ++ks) {
+                    if constexpr (BF) {
+                        qf[ks][j][0] = on ? *reinterpret_cast<const uint32_t*>(qh + ks * 16 + c2) : 0u;
+                        qf[ks][j][1] = on ? *reinterpret_cast<const uint32_t*>(qh + ks * 16 + c2 + 8) : 0u;
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float x = on ? qh[ks * 8 + c + 4 * e] : 0.f;
+                            if constexpr (SPLIT_Q) split_tf32(x, qf[ks][j][e], ql[ks][j][e]);
+                            else qf[ks][j][e] = __float_as_uint(x);
+                        }
+                    }
                 }
                 m[j][0] = m[j][1] = -INFINITY;
                 l[j][0] = l[j][1] = 0.f;
@@ -416,15 +449,42 @@ __global__ void __launch_bounds__(kWarps * 32, Plan<__nv_bfloat16, D>::kCtasPerS
             }
         }
         float s[NT][4] = {}, s2[NT][4] = {};  // two sums: half the chain of dependent products
+        if constexpr (BF) {
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ks += 2) {
-            uint32_t kf[2][4];
-            ldsm4(kf[0], kt + k_at + (((2 * ks + (mat >> 1)) ^ r8) << 4));
-            ldsm4(kf[1], kt + k_at + (((2 * ks + 2 + (mat >> 1)) ^ r8) << 4));
+            for (int ks = 0; ks < KS; ks += 2) {
+                uint32_t kf[2][4];
+                ldsm4(kf[0], kt + k_at + (((2 * ks + (mat >> 1)) ^ r8) << 4));
+                ldsm4(kf[1], kt + k_at + (((2 * ks + 2 + (mat >> 1)) ^ r8) << 4));
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                mma_bf16(s[j], kf[0], qf[ks][j][0], qf[ks][j][1]);
-                mma_bf16(s2[j], kf[1], qf[ks + 1][j][0], qf[ks + 1][j][1]);
+                for (int j = 0; j < NT; ++j) {
+                    mma_bf16(s[j], kf[0], qf[ks][j][0], qf[ks][j][1]);
+                    mma_bf16(s2[j], kf[1], qf[ks + 1][j][0], qf[ks + 1][j][1]);
+                }
+            }
+        } else {
+            // an 8 x 8 matrix of 16-bit elements is one of 8 rows x 4 32-bit ones: lane 4 r + x gets element x of row r
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                uint32_t x[4], hi[4], lo[4];
+                ldsm4(x, kt + k_at + (((2 * ks + (mat >> 1)) ^ r8) << 4));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) split_tf32(__uint_as_float(x[e]), hi[e], lo[e]);
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    uint32_t bh[2], bl[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        if constexpr (SPLIT_Q) {
+                            bh[e] = qf[ks][j][e];
+                            bl[e] = ql[ks][j][e];
+                        } else {
+                            split_tf32(__uint_as_float(qf[ks][j][e]), bh[e], bl[e]);
+                        }
+                    }
+                    mma_tf32(s2[j], lo, bh[0], bh[1]);
+                    mma_tf32(s2[j], hi, bl[0], bl[1]);
+                    mma_tf32(s[j], hi, bh[0], bh[1]);
+                }
             }
         }
         // scores in log2 units: elements 0, 1 are position g of heads c2, c2 + 1 (+ 8 j), elements 2, 3 position g + 8
@@ -457,9 +517,8 @@ __global__ void __launch_bounds__(kWarps * 32, Plan<__nv_bfloat16, D>::kCtasPerS
                     }
                 }
         }
-        uint32_t pf[NT][2];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
+        for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const float base = m[j][e] == -INFINITY ? 0.f : m[j][e];  // nothing attended so far: weights of 0
@@ -467,16 +526,52 @@ __global__ void __launch_bounds__(kWarps * 32, Plan<__nv_bfloat16, D>::kCtasPerS
                 s[j][e + 2] = exp2_fast(s[j][e + 2] - base);
                 l[j][e] += s[j][e] + s[j][e + 2];
             }
-            // the weights as the right operand (bf16, at most half a step off each; l sums them unrounded)
-            pf[j][0] = transpose8x8(pack_bf16(s[j][0], s[j][1]));
-            pf[j][1] = transpose8x8(pack_bf16(s[j][2], s[j][3]));
-        }
+        if constexpr (BF) {
+            uint32_t pf[NT][2];  // the weights as the right operand (at most half a step off each; l sums them unrounded)
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-            uint32_t vf[4];
-            ldsm4_trans(vf, vt + v_at + (((2 * i + (mat & 1)) ^ r8) << 4));
+            for (int j = 0; j < NT; ++j) {
+                pf[j][0] = transpose8x8(pack_bf16(s[j][0], s[j][1]));
+                pf[j][1] = transpose8x8(pack_bf16(s[j][2], s[j][3]));
+            }
 #pragma unroll
-            for (int j = 0; j < NT; ++j) mma_bf16(o[i][j], vf, pf[j][0], pf[j][1]);
+            for (int i = 0; i < D / 16; ++i) {
+                uint32_t vf[4];
+                ldsm4_trans(vf, vt + v_at + (((2 * i + (mat & 1)) ^ r8) << 4));
+#pragma unroll
+                for (int j = 0; j < NT; ++j) mma_bf16(o[i][j], vf, pf[j][0], pf[j][1]);
+            }
+        } else {
+            // Inner index x of the right operand stands for position 2 x (x < 4) or 2 (x - 4) + 1 of 8: lane 4 h + c holds
+            // head h's weights of positions 2 c and 2 c + 1. The same order in the left operand makes its loads free of
+            // bank conflicts: rows 0, 2, 4, 6 (and 1, 3, 5, 7) of the swizzled tile lie in different banks.
+            uint32_t ph[2][NT][2], pl[2][NT][2];
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int src = (c2 + e) * 4 + (g >> 1);
+                        const float x0 = __shfl_sync(~0u, s[j][2 * b], src), x1 = __shfl_sync(~0u, s[j][2 * b + 1], src);
+                        split_tf32(g & 1 ? x1 : x0, ph[b][j][e], pl[b][j][e]);
+                    }
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {  // elements 0, 1: channels g, g + 8 of position 2 c; 2, 3: of 2 c + 1
+                        const int r = b * 8 + c2 + (e >> 1), ch = i * 4 + (e & 1) * 2 + (g >> 2);
+                        split_tf32(lds_f32(vt + r * RB + ((ch ^ (r & 7)) << 4) + (g & 3) * 4), hi[e], lo[e]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        mma_tf32(o[i][j], lo, ph[b][j][0], ph[b][j][1]);
+                        mma_tf32(o[i][j], hi, pl[b][j][0], pl[b][j][1]);
+                        mma_tf32(o[i][j], hi, ph[b][j][0], ph[b][j][1]);
+                    }
+                }
         }
         if (bits & kEnds) {
             const int place = (int)(bits >> kPlaceShift);
@@ -492,14 +587,27 @@ __global__ void __launch_bounds__(kWarps * 32, Plan<__nv_bfloat16, D>::kCtasPerS
                 }
                 const int head = c2 + 8 * j;  // of element 0; element 1: the next
                 if (place == 2) {
-                    T* to = (T*)a.o + (size_t)(meta.x + g + 8 * j) * D + c2;
+                    if constexpr (BF) {
+                        T* to = (T*)a.o + (size_t)(meta.x + g + 8 * j) * D + c2;
 #pragma unroll
-                    for (int i = 0; i < D / 16; ++i) {  // transposed: lane 4 h + x holds channels 2 x, 2 x + 1 of head h
-                        const uint32_t lo = transpose8x8(pack_bf16(o[i][j][0] * inv[0], o[i][j][1] * inv[1]));
-                        const uint32_t hi = transpose8x8(pack_bf16(o[i][j][2] * inv[0], o[i][j][3] * inv[1]));
-                        if (g + 8 * j < heads) {
-                            *reinterpret_cast<uint32_t*>(to + i * 16) = lo;
-                            *reinterpret_cast<uint32_t*>(to + i * 16 + 8) = hi;
+                        for (int i = 0; i < D / 16; ++i) {  // transposed: lane 4 h + x holds channels 2 x, 2 x + 1 of head h
+                            const uint32_t lo = transpose8x8(pack_bf16(o[i][j][0] * inv[0], o[i][j][1] * inv[1]));
+                            const uint32_t hi = transpose8x8(pack_bf16(o[i][j][2] * inv[0], o[i][j][3] * inv[1]));
+                            if (g + 8 * j < heads) {
+                                *reinterpret_cast<uint32_t*>(to + i * 16) = lo;
+                                *reinterpret_cast<uint32_t*>(to + i * 16 + 8) = hi;
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            if (head + e >= heads) continue;
+                            float* to = (float*)a.o + (size_t)(meta.x + head + e) * D + g;
+#pragma unroll
+                            for (int i = 0; i < D / 16; ++i) {
+                                to[i * 16] = o[i][j][e] * inv[e];
+                                to[i * 16 + 8] = o[i][j][e + 2] * inv[e];
+                            }
                         }
                     }
                     if (a.lse && g < 2 && head + g < heads) {
@@ -615,68 +723,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(AttnDecodeAr
         a.lse[out] = sum == 0.f ? -INFINITY : fmaf(ref, kLn2, logf(sum));
 }
 
-template <typename T, int D>
-__global__ void attn_decode_kernel(AttnDecodeArgs a) {
-    constexpr int W = 4, E = D / 32;
-    __shared__ float so[W][D], sm[W], sl[W];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int n = blockIdx.x / a.Hq, h = blockIdx.x % a.Hq, hk = h / (a.Hq / a.Hk);
-    const int held = a.seq_lens[n], cap = a.max_pages * a.page_size;
-    const bool put = a.k_new && held >= 0;
-    // positions [first, last) are candidates; the new one, `held`, is the last of them
-    const long long total = held < 0 ? 0 : (long long)held + (put ? 1 : 0);  // a length near 2^31 must not wrap
-    const int last = (int)min(total, (long long)cap);
-    const int first = a.window ? (int)min(max(0ll, total - a.window), (long long)last) : 0;
-    const int* table = a.page_table + (size_t)n * a.max_pages;
-    const T* q = (const T*)a.q + ((size_t)n * a.Hq + h) * D;
-    float qv[E], acc[E], m = -INFINITY, l = 0.f;
-    for (int e = 0; e < E; ++e) {
-        qv[e] = to_f32(q[lane * E + e]) * a.scale;
-        acc[e] = 0.f;
-    }
-    for (int p = first + warp; p < last; p += W) {
-        const int page = table[p / a.page_size];
-        if (page < 0 || page >= a.n_pages) continue;
-        const size_t at = (((size_t)page * a.Hk + hk) * a.page_size + p % a.page_size) * D;
-        const T *kp = (const T*)a.k_cache + at, *vp = (const T*)a.v_cache + at;
-        if (put && p == held) {
-            kp = (const T*)a.k_new + ((size_t)n * a.Hk + hk) * D;
-            vp = (const T*)a.v_new + ((size_t)n * a.Hk + hk) * D;
-            if (h % (a.Hq / a.Hk) == 0)
-                for (int e = 0; e < E; ++e) {
-                    ((T*)a.k_cache)[at + lane * E + e] = kp[lane * E + e];
-                    ((T*)a.v_cache)[at + lane * E + e] = vp[lane * E + e];
-                }
-        }
-        float s = 0.f;
-        for (int e = 0; e < E; ++e) s = fmaf(qv[e], to_f32(kp[lane * E + e]), s);
-        s = warp_sum(s);
-        if (s == -INFINITY) continue;
-        const float top = fmaxf(m, s), keep = expf(m - top), p_ = expf(s - top);
-        l = l * keep + p_;
-        for (int e = 0; e < E; ++e) acc[e] = acc[e] * keep + p_ * to_f32(vp[lane * E + e]);
-        m = top;
-    }
-    for (int e = 0; e < E; ++e) so[warp][lane * E + e] = acc[e];
-    if (lane == 0) {
-        sm[warp] = m;
-        sl[warp] = l;
-    }
-    __syncthreads();
-    float top = -INFINITY, sum = 0.f;
-    for (int w = 0; w < W; ++w)
-        if (sl[w] != 0.f) top = fmaxf(top, sm[w]);
-    for (int w = 0; w < W; ++w)
-        if (sl[w] != 0.f) sum += sl[w] * expf(sm[w] - top);
-    for (int c = threadIdx.x; c < D; c += blockDim.x) {
-        float o = 0.f;
-        for (int w = 0; w < W; ++w)
-            if (sl[w] != 0.f) o += so[w][c] * expf(sm[w] - top);
-        ((T*)a.o)[((size_t)n * a.Hq + h) * D + c] = from_f32<T>(sum == 0.f ? 0.f : o / sum);
-    }
-    if (a.lse && threadIdx.x == 0) a.lse[(size_t)n * a.Hq + h] = sum == 0.f ? -INFINITY : top + logf(sum);
-}
-
 }  // namespace
 
 size_t attn_decode_workspace_bytes(int N, int Hq, int Hk, int d) {
@@ -709,18 +755,16 @@ static cudaError_t launch_attn(Kernel split, const AttnDecodeArgs& a, cudaStream
     return cudaLaunchKernelEx(&cfg, few ? attn_join_kernel<T, D, kJoinWarps> : attn_join_kernel<T, D, 1>, a, items);
 }
 
-template <int D>
-static cudaError_t launch_attn_bf16(const AttnDecodeArgs& a, cudaStream_t stream) {
-    if (a.Hq / a.Hk <= 8) return launch_attn<__nv_bfloat16, D>(attn_split_kernel<D, 1>, a, stream);
-    return launch_attn<__nv_bfloat16, D>(attn_split_kernel<D, 2>, a, stream);
+template <typename T, int D>
+static cudaError_t launch_attn_heads(const AttnDecodeArgs& a, cudaStream_t stream) {
+    if (a.Hq / a.Hk <= 8) return launch_attn<T, D>(attn_split_kernel<T, D, 1>, a, stream);
+    return launch_attn<T, D>(attn_split_kernel<T, D, 2>, a, stream);
 }
 
 cudaError_t launch_attn_decode(const AttnDecodeArgs& a, cudaStream_t stream) {
-    if (a.bf16) return a.d == 64 ? launch_attn_bf16<64>(a, stream) : launch_attn_bf16<128>(a, stream);
-    const unsigned blocks = (unsigned)a.N * a.Hq;
-    if (a.d == 64) attn_decode_kernel<float, 64><<<blocks, 128, 0, stream>>>(a);
-    else attn_decode_kernel<float, 128><<<blocks, 128, 0, stream>>>(a);
-    return cudaGetLastError();
+    if (a.bf16)
+        return a.d == 64 ? launch_attn_heads<__nv_bfloat16, 64>(a, stream) : launch_attn_heads<__nv_bfloat16, 128>(a, stream);
+    return a.d == 64 ? launch_attn_heads<float, 64>(a, stream) : launch_attn_heads<float, 128>(a, stream);
 }
 
 }  // namespace kda
