@@ -117,7 +117,7 @@ def _check(fn: str, code: int):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _dtype_of(t) -> str:
@@ -133,8 +133,26 @@ def _stream(stream, device=None):
     """The stream handle to pass: the given torch stream, else the current
     stream of `device` (the tensors' device), else of the current device."""
     import torch
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is None:
+        # the handle alone where torch offers it: building a Stream object costs 2 us a call
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None and device is not None and device.index is not None:
+            return raw(device.index)
+        stream = torch.cuda.current_stream(device)
+    return stream.cuda_stream
+
+
+class _Here:
+    """Stands for torch.cuda.device where the device is the current one already."""
+
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE = _Here()
 
 
 def _on(device):
@@ -142,10 +160,14 @@ def _on(device):
     the current device (and the allocation-free entry point looks up its
     scratch array there), so it must be the device the pointers live on."""
     import torch
+    if device is not None and device.index is not None and device.index == torch.cuda.current_device():
+        return _HERE
     return torch.cuda.device(device)
 
 
 def _need(t, name, shape, dtype, device):
+    if t.dtype == dtype and t.shape == shape and t.is_contiguous() and t.device == device and t.is_cuda:
+        return
     if not t.is_cuda:
         raise ValueError(f"{name}: must be a CUDA tensor (this library has no CPU path)")
     if t.device != device or t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():

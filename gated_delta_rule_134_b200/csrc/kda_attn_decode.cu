@@ -22,6 +22,8 @@
 // pair and does not end it. attn_join_kernel joins the pieces in order. A warp
 // works for itself (no block barrier in the loop): it copies 16 rows of K and V
 // a stage with 16-byte cp.async, several stages ahead, across the ends of pairs.
+#include <atomic>
+
 #include "kda_common.cuh"
 #include "kda_internal.h"
 #include "kda_sm100.cuh"
@@ -732,12 +734,22 @@ size_t attn_decode_workspace_bytes(int N, int Hq, int Hk, int d) {
     return (size_t)((char*)(p.pair + (size_t)N * Hk * blocks) - (char*)nullptr);
 }
 
-template <typename T, int D, typename Kernel>
-static cudaError_t launch_attn(Kernel split, const AttnDecodeArgs& a, cudaStream_t stream) {
+template <typename T, int D, int NT>
+static cudaError_t launch_attn(const AttnDecodeArgs& a, cudaStream_t stream) {
     using Geo = Geometry<T, D>;
+    auto split = attn_split_kernel<T, D, NT>;
     const int G = a.Hq / a.Hk, pairs = a.N * a.Hk * ((G + kHeads - 1) / kHeads);
-    cudaError_t err = cudaFuncSetAttribute(split, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo::kSmem);
+    // The shared-memory limit is set once a device (a bit each; devices past 63 set it every time).
+    static std::atomic<unsigned long long> raised{0};
+    int device = 0;
+    cudaError_t err = cudaGetDevice(&device);
     if (err != cudaSuccess) return err;
+    const unsigned long long bit = device < 64 ? 1ull << device : 0;
+    if (!(raised.load(std::memory_order_relaxed) & bit)) {
+        err = cudaFuncSetAttribute(split, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo::kSmem);
+        if (err != cudaSuccess) return err;
+        raised.fetch_or(bit, std::memory_order_relaxed);
+    }
     split<<<Geo::kCtas, kWarps * 32, Geo::kSmem, stream>>>(a);
     if ((err = cudaGetLastError()) != cudaSuccess) return err;
     // The join is launched while the split kernel runs (programmatic dependent launch) and waits for its end.
@@ -757,8 +769,7 @@ static cudaError_t launch_attn(Kernel split, const AttnDecodeArgs& a, cudaStream
 
 template <typename T, int D>
 static cudaError_t launch_attn_heads(const AttnDecodeArgs& a, cudaStream_t stream) {
-    if (a.Hq / a.Hk <= 8) return launch_attn<T, D>(attn_split_kernel<T, D, 1>, a, stream);
-    return launch_attn<T, D>(attn_split_kernel<T, D, 2>, a, stream);
+    return a.Hq / a.Hk <= 8 ? launch_attn<T, D, 1>(a, stream) : launch_attn<T, D, 2>(a, stream);
 }
 
 cudaError_t launch_attn_decode(const AttnDecodeArgs& a, cudaStream_t stream) {
