@@ -1,9 +1,20 @@
 // Queries and keys of a layer: norm per head and rotation by position in one
-// pass, and the backward pass. One warp per (token, head).
+// pass, and the backward pass.
 //
-//     y = R (w x r),  r = (m + eps)^-1/2,  m = share * sum x^2
-// (share = 1 for the L2 norm, 1/d for the RMS norm.) With u = R^T dy, n = x r:
+//     y = R (w x r),  r = (share * sum x^2 + eps)^-1/2      (share: 1 for L2, 1/d for RMS)
+// With u = R^T dy, n = x r:
 //     dw = sum u n,   dx = r (w u - share * n * sum(w u n)).
+//
+// What bounds it: HBM, 2 (backward 3) elements of the tensors per channel. A
+// head is read once by a group of LANES lanes, 8 channels (16 or 32 bytes) a
+// lane, and stays in registers: the sums are shuffles within the group, and the
+// rotation's partner channel is either in the same lane (interleaved pairs) or,
+// unnormalised, in the lane rot/16 away (halves). A group takes up to `chunk`
+// heads of one token, so that the token's row of the tables, with the weight
+// multiplied in, is read once for them all.
+#include <algorithm>
+#include <type_traits>
+
 #include "kda_common.cuh"
 #include "kda_internal.h"
 
@@ -11,156 +22,397 @@ namespace kda {
 
 namespace {
 
+constexpr int kThreads = 256;
+enum { kNoTurn = 0, kHalves = 1, kPairs = 2 };
+
+// One side (queries or keys) of a call.
 struct Side {
     const void *x, *w, *dy;
     void* y;
-    float* dw;
     long long stride_t, stride_h;
     int H;
     float scale;
 };
+
+__device__ __forceinline__ Side side_of(const QkArgs& a, bool is_q) {
+    return is_q ? Side{a.q, a.q_weight, a.d_q_out, a.q_out, a.q_stride_t, a.q_stride_h, a.Hq, a.q_scale}
+                : Side{a.k, a.k_weight, a.d_k_out, a.k_out, a.k_stride_t, a.k_stride_h, a.Hk, 1.f};
+}
+
+// 8 channels as they lie in memory.
+template <typename T> struct Raw {
+    static constexpr int W = 8 * sizeof(T) / 4;
+    uint32_t w[W];
+    __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+        for (int i = 0; i < W; i += 4) {
+            const uint4 v = reinterpret_cast<const uint4*>(p)[i / 4];
+            w[i] = v.x; w[i + 1] = v.y; w[i + 2] = v.z; w[i + 3] = v.w;
+        }
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i] = 0u;
+    }
+    __device__ __forceinline__ float get(int i) const {
+        if constexpr (W == 8) return __uint_as_float(w[i]);
+        else return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+    }
+};
+
+__device__ __forceinline__ void store8(float* p, const float (&y)[8]) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(y[0], y[1], y[2], y[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(y[4], y[5], y[6], y[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&y)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <int LANES> __device__ __forceinline__ float group_sum(float x) {
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+    return x;
+}
+
+// r of a head from its sum of squares. Where that leaves 32 bits the head is
+// rescaled by 2^-80 first (eps is then far below the sum).
+template <typename T, int LANES>
+__device__ __forceinline__ float rnorm(const Raw<T>& x, float ss, float share, float eps) {
+    float r = rsqrtf(fmaf(ss, share, eps));
+    const bool out = !(ss < 1e37f);
+    if (__any_sync(~0u, out)) {
+        float s = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s = fmaf(x.get(e) * 0x1p-80f, x.get(e) * 0x1p-80f, s);
+        s = group_sum<LANES>(s);
+        if (out) r = 0x1p-80f * rsqrtf(s * share);
+    }
+    return r;
+}
 
 __device__ __forceinline__ long long position_of(const QkArgs& a, long long t) {
     const long long p = a.pos_bytes == 8 ? ((const long long*)a.positions)[t] : (long long)((const int*)a.positions)[t];
     return min(max(p, 0ll), (long long)a.max_pos - 1);
 }
 
-// Partner channel, and this channel's cosine and signed sine: y_c = x_c cos + x_partner sin.
-__device__ __forceinline__ int turn(const QkArgs& a, long long pos, int c, float& cs, float& sn) {
+// This lane's cosines and sines, the sines signed as in y_c = x_c cos + x_partner sin
+// (1 and 0 for channels that are not rotated). Returns the lane that holds the partners.
+template <int MODE>
+__device__ __forceinline__ int turn_of(const QkArgs& a, long long t, int c, int lane, float (&cs)[8], float (&sn)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        cs[e] = 1.f;
+        sn[e] = 0.f;
+    }
+    if (MODE == kNoTurn || c >= a.rot) return lane;
     const int half = a.rot / 2;
-    cs = 1.f;
-    sn = 0.f;
-    if (c >= a.rot) return c;
-    const int i = a.interleaved ? c / 2 : c % half;
-    const bool first = a.interleaved ? c % 2 == 0 : c < half;
-    cs = a.cos[pos * half + i];
-    sn = a.sin[pos * half + i];
-    if (first) sn = -sn;
-    return a.interleaved ? (c ^ 1) : (first ? c + half : c - half);
+    const size_t row = (size_t)position_of(a, t) * half;
+    if (MODE == kHalves) {
+        const bool first = c < half;
+        const int i = first ? c : c - half;
+        const float4 *pc = reinterpret_cast<const float4*>(a.cos + row + i), *ps = reinterpret_cast<const float4*>(a.sin + row + i);
+        const float4 c0 = __ldg(pc), c1 = __ldg(pc + 1), s0 = __ldg(ps), s1 = __ldg(ps + 1);
+        cs[0] = c0.x; cs[1] = c0.y; cs[2] = c0.z; cs[3] = c0.w; cs[4] = c1.x; cs[5] = c1.y; cs[6] = c1.z; cs[7] = c1.w;
+        sn[0] = s0.x; sn[1] = s0.y; sn[2] = s0.z; sn[3] = s0.w; sn[4] = s1.x; sn[5] = s1.y; sn[6] = s1.z; sn[7] = s1.w;
+        if (first) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sn[e] = -sn[e];
+        }
+        return first ? lane + half / 8 : lane - half / 8;
+    }
+    const float4 c0 = __ldg(reinterpret_cast<const float4*>(a.cos + row + c / 2)), s0 = __ldg(reinterpret_cast<const float4*>(a.sin + row + c / 2));
+    const float cc[4] = {c0.x, c0.y, c0.z, c0.w}, ss[4] = {s0.x, s0.y, s0.z, s0.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        cs[e] = cc[e / 2];
+        sn[e] = e % 2 ? ss[e / 2] : -ss[e / 2];
+    }
+    return lane;
 }
 
-__device__ __forceinline__ float rnorm(const float* x, int d, float share, float eps) {
-    float top = 0.f, ss = 0.f;
-    const int lane = threadIdx.x & 31;
-    for (int c = lane; c < d; c += 32) top = fmaxf(top, fabsf(x[c]));
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-    const float down = top > 1e15f ? 0x1p-80f : 1.f;
-    for (int c = lane; c < d; c += 32) ss = fmaf(x[c] * down, x[c] * down, ss);
-    ss = warp_sum(ss);
-    return down * rsqrtf(fmaf(ss, share, eps * down * down));
+// The partner channels of x, unnormalised.
+template <typename T, int MODE> __device__ __forceinline__ Raw<T> partners(const Raw<T>& x, int from) {
+    Raw<T> p = x;
+    if constexpr (MODE == kHalves) {
+#pragma unroll
+        for (int i = 0; i < Raw<T>::W; ++i) p.w[i] = __shfl_sync(~0u, x.w[i], from);
+    } else if constexpr (MODE == kPairs) {
+        if constexpr (Raw<T>::W == 8) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) p.w[i] = x.w[i ^ 1];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p.w[i] = __funnelshift_l(x.w[i], x.w[i], 16);
+        }
+    }
+    return p;
 }
 
-template <typename T>
-__global__ void qk_fwd_kernel(QkArgs a) {
-    __shared__ float sx[4][256];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, H = a.Hq + a.Hk;
-    const long long row = (long long)blockIdx.x * 4 + warp;
-    if (row >= (long long)a.n * H) return;
-    const long long t = row / H;
-    int h = (int)(row % H);
-    const bool is_q = h < a.Hq;
-    if (!is_q) h -= a.Hq;
-    const T* x = is_q ? (const T*)a.q + t * a.q_stride_t + h * a.q_stride_h
-                      : (const T*)a.k + t * a.k_stride_t + h * a.k_stride_h;
-    T* y = is_q ? (T*)a.q_out + (t * a.Hq + h) * a.d : (T*)a.k_out + (t * a.Hk + h) * a.d;
-    const T* w = (const T*)(is_q ? a.q_weight : a.k_weight);
-    float* s = sx[warp];
-    for (int c = lane; c < a.d; c += 32) s[c] = to_f32(x[c]);
-    __syncwarp();
-    const float r = rnorm(s, a.d, a.norm ? 1.f / a.d : 1.f, a.eps);
-    __syncwarp();
-    for (int c = lane; c < a.d; c += 32) s[c] = s[c] * r * (w ? to_f32(w[c]) : 1.f);
-    __syncwarp();
-    const long long pos = a.positions ? position_of(a, t) : 0;
-    for (int c = lane; c < a.d; c += 32) {
-        float cs, sn;
-        const int p = turn(a, pos, c, cs, sn);
-        y[c] = from_f32<T>((s[c] * cs + s[p] * sn) * (is_q ? a.q_scale : 1.f));
+template <typename T, int LANES, int MODE>
+__global__ void __launch_bounds__(kThreads) qk_fwd_kernel(QkArgs a, int chunk, int q_chunks, int chunks) {
+    constexpr int GROUPS = kThreads / LANES, AHEAD = 4;
+    const int lane = threadIdx.x & 31, c = (threadIdx.x % LANES) * 8;
+    const long long item = (long long)blockIdx.x * GROUPS + threadIdx.x / LANES;
+    const long long t = item / chunks;
+    const int part = (int)(item % chunks);
+    const bool live = t < a.n, is_q = part < q_chunks, mine = live && c < a.d;
+    const Side s = side_of(a, is_q);
+    const int h0 = (is_q ? part : part - q_chunks) * chunk, heads = live ? min(chunk, s.H - h0) : 0;
+    const T* x = (const T*)s.x + (live ? t * s.stride_t + h0 * s.stride_h : 0) + c;
+    T* y = (T*)s.y + (live ? (t * s.H + h0) * a.d : 0) + c;
+    Raw<T> v[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+        v[i].clear();
+        if (mine && i < heads) v[i].load(x + i * s.stride_h);
+    }
+    float cw[8], sw[8];  // cosine and signed sine, times the weight of the channel they meet and the side's scale
+    int from = lane;
+    if (mine) from = turn_of<MODE>(a, t, c, lane, cw, sw);
+    else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) cw[e] = sw[e] = 0.f;
+    }
+    // A warp may hold groups of both sides, of which one alone has a weight: the exchange is outside of any condition.
+    Raw<T> w;
+    w.clear();
+    if (mine && s.w) w.load((const T*)s.w + c);
+    const Raw<T> wp = partners<T, MODE>(w, from);
+    if (s.w) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            cw[e] *= w.get(e);
+            sw[e] *= wp.get(e);
+        }
+    }
+    if (s.scale != 1.f) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            cw[e] *= s.scale;
+            sw[e] *= s.scale;
+        }
+    }
+    const float share = a.norm ? 1.f / a.d : 1.f;
+    // every lane of a warp runs as many rounds as its longest group: the shuffles take all of them
+    const int rounds = __reduce_max_sync(~0u, heads);
+    for (int h = 0; h < rounds; h += AHEAD) {
+        Raw<T> u[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            u[i] = v[i];
+            if (mine && h + AHEAD + i < heads) v[i].load(x + (h + AHEAD + i) * s.stride_h);
+        }
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            if (h + i >= rounds) break;
+            float ss = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) ss = fmaf(u[i].get(e), u[i].get(e), ss);
+            ss = group_sum<LANES>(ss);
+            const float r = rnorm<T, LANES>(u[i], ss, share, a.eps);
+            const Raw<T> p = partners<T, MODE>(u[i], from);
+            float out[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float z = u[i].get(e) * r * cw[e];
+                out[e] = MODE == kNoTurn ? z : fmaf(p.get(e) * r, sw[e], z);
+            }
+            if (mine && h + i < heads) store8(y + (long long)(h + i) * a.d, out);
+        }
     }
 }
 
-// One CTA walks rows (token, head) of one side with a stride; dw partials per CTA.
-template <typename T>
-__global__ void qk_bwd_kernel(QkArgs a, float* part) {
-    __shared__ float su[4][256], sn_[4][256], sw[4][256];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const bool is_q = blockIdx.y == 0;
-    const int H = is_q ? a.Hq : a.Hk;
-    const T* w = (const T*)(is_q ? a.q_weight : a.k_weight);
-    float* u = su[warp];
-    float* n = sn_[warp];
-    float* dw = sw[warp];
+// CTAs below q_ctas walk the queries, the others the keys, each group a chunk of heads of a token at a time; `part`
+// gets each CTA's sum of the weight's gradient.
+template <typename T, int LANES, int MODE>
+__global__ void __launch_bounds__(kThreads, 2) qk_bwd_kernel(QkArgs a, int chunk, int q_ctas, float* part) {
+    constexpr int GROUPS = kThreads / LANES;
+    __shared__ float s_dw[kThreads / 32][LANES * 8];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // qk_dw_kernel: waits for this grid's end
+    const int lane = threadIdx.x & 31, c = (threadIdx.x % LANES) * 8;
+    const bool is_q = (int)blockIdx.x < q_ctas, on = c < a.d;
+    const Side s = side_of(a, is_q);
+    const int cta = is_q ? blockIdx.x : blockIdx.x - q_ctas, ctas = is_q ? q_ctas : gridDim.x - q_ctas;
+    const int chunks = (s.H + chunk - 1) / chunk;
+    const long long items = (long long)a.n * chunks;
     const float share = a.norm ? 1.f / a.d : 1.f;
-    for (int c = lane; c < a.d; c += 32) dw[c] = 0.f;
-    for (long long row = (long long)blockIdx.x * 4 + warp; row < (long long)a.n * H; row += (long long)gridDim.x * 4) {
-        const long long t = row / H;
-        const int h = (int)(row % H);
-        const T* x = is_q ? (const T*)a.q + t * a.q_stride_t + h * a.q_stride_h
-                          : (const T*)a.k + t * a.k_stride_t + h * a.k_stride_h;
-        const T* dy = (const T*)(is_q ? a.d_q_out : a.d_k_out) + row * a.d;
-        T* dx = (T*)(is_q ? a.q_out : a.k_out) + row * a.d;
-        const long long pos = a.positions ? position_of(a, t) : 0;
-        __syncwarp();
-        for (int c = lane; c < a.d; c += 32) {
-            n[c] = to_f32(x[c]);
-            float cs, sn;
-            const int p = turn(a, pos, c, cs, sn);
-            u[c] = (to_f32(dy[c]) * cs - to_f32(dy[p]) * sn) * (is_q ? a.q_scale : 1.f);
+    Raw<T> w;
+    w.clear();
+    if (s.w && on) w.load((const T*)s.w + c);
+    float dw[8] = {};
+    // the bound is the same for all groups of a CTA: the shuffles take whole warps
+    for (long long base = (long long)cta * GROUPS; base < items; base += (long long)ctas * GROUPS) {
+        const long long item = base + threadIdx.x / LANES;
+        const bool live = item < items, mine = live && on;
+        const long long t = live ? item / chunks : 0;
+        const int h0 = (int)(item % chunks) * chunk, heads = live ? min(chunk, s.H - h0) : 0;
+        const T* x = (const T*)s.x + t * s.stride_t + (live ? h0 * s.stride_h : 0) + c;
+        const long long out = (live ? (t * s.H + h0) * a.d : 0) + c;
+        const T* dy = (const T*)s.dy + out;
+        T* dx = (T*)s.y + out;
+        Raw<T> vx, vy;
+        vx.clear();
+        vy.clear();
+        if (mine && heads > 0) {
+            vx.load(x);
+            vy.load(dy);
         }
-        __syncwarp();
-        const float r = rnorm(n, a.d, share, a.eps);
-        __syncwarp();
-        float dot = 0.f;
-        for (int c = lane; c < a.d; c += 32) {
-            n[c] *= r;
-            dw[c] = fmaf(u[c], n[c], dw[c]);
-            u[c] *= w ? to_f32(w[c]) : 1.f;
-            dot = fmaf(u[c], n[c], dot);
+        float cs[8], sn[8];
+        int from = lane;
+        if (mine) from = turn_of<MODE>(a, t, c, lane, cs, sn);
+        else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) cs[e] = sn[e] = 0.f;
         }
-        dot = warp_sum(dot) * share;
-        for (int c = lane; c < a.d; c += 32) dx[c] = from_f32<T>(r * (u[c] - n[c] * dot));
+        const int rounds = __reduce_max_sync(~0u, heads);
+        for (int h = 0; h < rounds; ++h) {
+            const Raw<T> ux = vx, uy = vy;
+            if (mine && h + 1 < heads) {
+                vx.load(x + (h + 1) * s.stride_h);
+                vy.load(dy + (long long)(h + 1) * a.d);
+            }
+            const bool do_it = mine && h < heads;
+            const Raw<T> p = partners<T, MODE>(uy, from);
+            float u[8], ss = 0.f, dot = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {  // u = R^T dy: the same cosine, the sine with the other sign
+                u[e] = uy.get(e) * cs[e];
+                if (MODE != kNoTurn) u[e] = fmaf(p.get(e), -sn[e], u[e]);
+                u[e] *= s.scale;
+                ss = fmaf(ux.get(e), ux.get(e), ss);
+            }
+            ss = group_sum<LANES>(ss);
+            const float r = rnorm<T, LANES>(ux, ss, share, a.eps);
+            float n[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                n[e] = ux.get(e) * r;
+                if (do_it) dw[e] = fmaf(u[e], n[e], dw[e]);
+                if (s.w) u[e] *= w.get(e);
+                dot = fmaf(u[e], n[e], dot);
+            }
+            dot = group_sum<LANES>(dot) * share;
+            float o[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = r * fmaf(-n[e], dot, u[e]);
+            if (do_it) store8(dx + (long long)h * a.d, o);
+        }
+    }
+    if (!part) return;
+    // groups of the warp, then warps, then (qk_dw_kernel) CTAs
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+#pragma unroll
+        for (int o = LANES; o < 32; o <<= 1) dw[e] += __shfl_xor_sync(~0u, dw[e], o);
+    if (lane < LANES) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s_dw[threadIdx.x / 32][c + e] = dw[e];
     }
     __syncthreads();
-    if (!part) return;
-    for (int c = threadIdx.x; c < a.d; c += blockDim.x)
-        part[((size_t)blockIdx.y * gridDim.x + blockIdx.x) * a.d + c] = (sw[0][c] + sw[1][c]) + (sw[2][c] + sw[3][c]);
-}
-
-__global__ void qk_dw_kernel(const float* part, float* dwq, float* dwk, int blocks, int d) {
-    float* dw = blockIdx.x == 0 ? dwq : dwk;
-    if (!dw) return;
-    for (int c = threadIdx.x; c < d; c += blockDim.x) {
-        double s = 0;
-        for (int b = 0; b < blocks; ++b) s += part[((size_t)blockIdx.x * blocks + b) * d + c];
-        dw[c] = (float)s;
+    for (int i = threadIdx.x; i < a.d; i += kThreads) {
+        float sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < kThreads / 32; ++k) sum += s_dw[k][i];
+        part[(size_t)blockIdx.x * a.d + i] = sum;
     }
 }
 
-constexpr int kBwdBlocks = 592;
+// Sums the CTAs' parts, in a fixed order: block (side, 32 channels), 32 rows of threads.
+__global__ void __launch_bounds__(1024) qk_dw_kernel(const float* part, float* dwq, float* dwk, int q_ctas, int ctas, int d) {
+    __shared__ float s[32][33];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    float* dw = blockIdx.x == 0 ? dwq : dwk;
+    if (!dw) return;
+    const int x = threadIdx.x & 31, y = threadIdx.x >> 5, c = blockIdx.y * 32 + x;
+    const int b = blockIdx.x == 0 ? 0 : q_ctas, e = blockIdx.x == 0 ? q_ctas : ctas;
+    float sum = 0.f;
+    if (c < d)
+        for (int i = b + y; i < e; i += 32) sum += part[(size_t)i * d + c];
+    s[y][x] = sum;
+    __syncthreads();
+    sum = warp_sum(s[x][y]);  // channel y of the block
+    if (x == 0 && blockIdx.y * 32 + y < d) dw[blockIdx.y * 32 + y] = sum;
+}
+
+constexpr int kBwdCtas = 592;
+
+template <typename F> cudaError_t with_lanes(int d, F f) {
+    if (d <= 8) return f(std::integral_constant<int, 1>());
+    if (d <= 16) return f(std::integral_constant<int, 2>());
+    if (d <= 32) return f(std::integral_constant<int, 4>());
+    if (d <= 64) return f(std::integral_constant<int, 8>());
+    if (d <= 128) return f(std::integral_constant<int, 16>());
+    return f(std::integral_constant<int, 32>());
+}
+template <typename F> cudaError_t with_mode(const QkArgs& a, F f) {
+    if (!a.positions) return f(std::integral_constant<int, kNoTurn>());
+    return a.interleaved ? f(std::integral_constant<int, kPairs>()) : f(std::integral_constant<int, kHalves>());
+}
 
 }  // namespace
 
 size_t qk_norm_rope_bwd_workspace_bytes(int n, int Hq, int Hk, int d) {
     (void)n; (void)Hq; (void)Hk;
-    return (size_t)2 * kBwdBlocks * d * sizeof(float);
+    return (size_t)kBwdCtas * d * sizeof(float);
 }
 
 cudaError_t launch_qk_norm_rope(const QkArgs& a, cudaStream_t stream) {
-    const unsigned blocks = (unsigned)(((long long)a.n * (a.Hq + a.Hk) + 3) / 4);
-    if (a.bf16) qk_fwd_kernel<__nv_bfloat16><<<blocks, 128, 0, stream>>>(a);
-    else qk_fwd_kernel<float><<<blocks, 128, 0, stream>>>(a);
-    return cudaGetLastError();
+    return with_lanes(a.d, [&](auto lanes) {
+        return with_mode(a, [&](auto mode) {
+            constexpr int L = decltype(lanes)::value, M = decltype(mode)::value, GROUPS = kThreads / L;
+            // heads of a group: 8 where that still gives every SM 32 warps, fewer for few tokens
+            int chunk = 8;
+            auto items = [&] { return (long long)a.n * ((a.Hq + chunk - 1) / chunk + (a.Hk + chunk - 1) / chunk); };
+            while (chunk > 1 && items() * L < 148ll * 1024) chunk /= 2;
+            const int q_chunks = (a.Hq + chunk - 1) / chunk, chunks = q_chunks + (a.Hk + chunk - 1) / chunk;
+            const unsigned blocks = (unsigned)((items() + GROUPS - 1) / GROUPS);
+            if (a.bf16) qk_fwd_kernel<__nv_bfloat16, L, M><<<blocks, kThreads, 0, stream>>>(a, chunk, q_chunks, chunks);
+            else qk_fwd_kernel<float, L, M><<<blocks, kThreads, 0, stream>>>(a, chunk, q_chunks, chunks);
+            return cudaGetLastError();
+        });
+    });
 }
 
 cudaError_t launch_qk_norm_rope_bwd(const QkArgs& a, cudaStream_t stream) {
     float* part = a.d_q_weight || a.d_k_weight ? (float*)a.workspace : nullptr;
-    const dim3 grid(kBwdBlocks, 2);
-    if (a.bf16) qk_bwd_kernel<__nv_bfloat16><<<grid, 128, 0, stream>>>(a, part);
-    else qk_bwd_kernel<float><<<grid, 128, 0, stream>>>(a, part);
-    const cudaError_t err = cudaGetLastError();
+    int q_ctas = 0, ctas = 0;
+    const cudaError_t err = with_lanes(a.d, [&](auto lanes) {
+        return with_mode(a, [&](auto mode) {
+            constexpr int L = decltype(lanes)::value, M = decltype(mode)::value, GROUPS = kThreads / L;
+            int chunk = 4;
+            auto items = [&](int H) { return (long long)a.n * ((H + chunk - 1) / chunk); };
+            while (chunk > 1 && (items(a.Hq) + items(a.Hk)) * L < 148ll * 1024) chunk /= 2;
+            // CTAs of each side in the ratio of their heads, no more than there is work for
+
+            const int all = a.Hq + a.Hk;
+            q_ctas = all ? (int)std::min((long long)(kBwdCtas - 1) * a.Hq / all + (a.Hq > 0), (items(a.Hq) + GROUPS - 1) / GROUPS) : 0;
+
+            const int k_ctas = (int)std::min((long long)(kBwdCtas - q_ctas), (items(a.Hk) + GROUPS - 1) / GROUPS);
+            ctas = q_ctas + k_ctas;
+            if (ctas == 0) return cudaSuccess;
+            if (a.bf16) qk_bwd_kernel<__nv_bfloat16, L, M><<<ctas, kThreads, 0, stream>>>(a, chunk, q_ctas, part);
+            else qk_bwd_kernel<float, L, M><<<ctas, kThreads, 0, stream>>>(a, chunk, q_ctas, part);
+            return cudaGetLastError();
+        });
+    });
     if (err != cudaSuccess || !part) return err;
-    qk_dw_kernel<<<2, 256, 0, stream>>>(part, a.d_q_weight, a.d_k_weight, kBwdBlocks, a.d);
-    return cudaGetLastError();
+    // launched while the first kernel runs; it waits for its end there
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2, (a.d + 31) / 32);
+    cfg.blockDim = dim3(1024);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, qk_dw_kernel, (const float*)part, a.d_q_weight, a.d_k_weight, q_ctas, ctas, a.d);
 }
 
 }  // namespace kda
