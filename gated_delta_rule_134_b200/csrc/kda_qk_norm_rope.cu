@@ -50,6 +50,13 @@ template <typename T> struct Raw {
             w[i] = v.x; w[i + 1] = v.y; w[i + 2] = v.z; w[i + 3] = v.w;
         }
     }
+    __device__ __forceinline__ void load_pieces(const uint4* p, int apart) {
+#pragma unroll
+        for (int i = 0; i < W; i += 4) {
+            const uint4 v = p[i / 4 * apart];
+            w[i] = v.x; w[i + 1] = v.y; w[i + 2] = v.z; w[i + 3] = v.w;
+        }
+    }
     __device__ __forceinline__ void clear() {
 #pragma unroll
         for (int i = 0; i < W; ++i) w[i] = 0u;
@@ -58,6 +65,7 @@ template <typename T> struct Raw {
         if constexpr (W == 8) return __uint_as_float(w[i]);
         else return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
     }
+    __device__ __forceinline__ F2 pair(int i) const { return f2(get(2 * i), get(2 * i + 1)); }
 };
 
 __device__ __forceinline__ void store8(float* p, const float (&y)[8]) {
@@ -104,7 +112,7 @@ __device__ __forceinline__ long long position_of(const QkArgs& a, long long t) {
 // This lane's cosines and sines, the sines signed as in y_c = x_c cos + x_partner sin
 // (1 and 0 for channels that are not rotated). Returns the lane that holds the partners.
 template <int MODE>
-__device__ __forceinline__ int turn_of(const QkArgs& a, long long t, int c, int lane, float (&cs)[8], float (&sn)[8]) {
+__device__ __forceinline__ int turn_of(const QkArgs& a, long long pos, int c, int lane, float (&cs)[8], float (&sn)[8]) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         cs[e] = 1.f;
@@ -112,7 +120,7 @@ __device__ __forceinline__ int turn_of(const QkArgs& a, long long t, int c, int 
     }
     if (MODE == kNoTurn || c >= a.rot) return lane;
     const int half = a.rot / 2;
-    const size_t row = (size_t)position_of(a, t) * half;
+    const size_t row = (size_t)pos * half;
     if (MODE == kHalves) {
         const bool first = c < half;
         const int i = first ? c : c - half;
@@ -174,7 +182,7 @@ __global__ void __launch_bounds__(kThreads) qk_fwd_kernel(QkArgs a, int chunk, i
     }
     float cw[8], sw[8];  // cosine and signed sine, times the weight of the channel they meet and the side's scale
     int from = lane;
-    if (mine) from = turn_of<MODE>(a, t, c, lane, cw, sw);
+    if (mine) from = turn_of<MODE>(a, MODE == kNoTurn ? 0 : position_of(a, t), c, lane, cw, sw);
     else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) cw[e] = sw[e] = 0.f;
@@ -228,98 +236,161 @@ __global__ void __launch_bounds__(kThreads) qk_fwd_kernel(QkArgs a, int chunk, i
     }
 }
 
-// CTAs below q_ctas walk the queries, the others the keys, each group a chunk of heads of a token at a time; `part`
-// gets each CTA's sum of the weight's gradient.
+// CTAs below q_ctas walk the queries, the others the keys. A side's heads are cut into `parts` of `chunk` (the last may
+// hold fewer); a group keeps to one part and walks the tokens with a stride. Loads run AHEAD heads before the
+// arithmetic, across the tokens. `part_sums` gets each CTA's sum of the weight's gradient. The arithmetic is on
+// pairs of channels (one instruction for two products), without which the kernel would be bound by its instructions.
+template <typename T> struct BwdPlan {
+    static constexpr int kRowBytes = 8 * sizeof(T);                 // a thread's channels of one head
+    static constexpr int kStages = 8 / (sizeof(T) / 2);             // heads in flight
+    static constexpr int kSmem = kStages * 2 * kRowBytes * kThreads;  // 64 KB
+};
+
 template <typename T, int LANES, int MODE>
-__global__ void __launch_bounds__(kThreads, 2) qk_bwd_kernel(QkArgs a, int chunk, int q_ctas, float* part) {
-    constexpr int GROUPS = kThreads / LANES;
-    __shared__ float s_dw[kThreads / 32][LANES * 8];
+__global__ void __launch_bounds__(kThreads, 2) qk_bwd_kernel(QkArgs a, int q_chunk, int k_chunk, int q_ctas, float* part_sums) {
+    using Plan = BwdPlan<T>;
+    constexpr int GROUPS = kThreads / LANES, S = Plan::kStages, W = Plan::kRowBytes / 16;
+    extern __shared__ __align__(16) uint4 ring[];  // [stage][x, dy][16-byte piece][thread]: read by the thread that filled it
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // qk_dw_kernel: waits for this grid's end
     const int lane = threadIdx.x & 31, c = (threadIdx.x % LANES) * 8;
-    const bool is_q = (int)blockIdx.x < q_ctas, on = c < a.d;
+    const bool is_q = (int)blockIdx.x < q_ctas;
     const Side s = side_of(a, is_q);
     const int cta = is_q ? blockIdx.x : blockIdx.x - q_ctas, ctas = is_q ? q_ctas : gridDim.x - q_ctas;
-    const int chunks = (s.H + chunk - 1) / chunk;
-    const long long items = (long long)a.n * chunks;
+    const int chunk = is_q ? q_chunk : k_chunk, parts = (s.H + chunk - 1) / chunk;
+    const int group = cta * GROUPS + threadIdx.x / LANES;
+    const int stride = max(ctas * GROUPS / parts, 1);  // tokens that are worked on at once
+    const int part = group % parts, t0 = group / parts, h0 = part * chunk;
+    const bool on = c < a.d && t0 < stride;
+    const int heads = on ? min(chunk, s.H - h0) : 0;
+    const int rounds = (int)(((long long)a.n + stride - 1) / stride);  // the same for all groups: the shuffles take whole warps
+    const long long steps = (long long)rounds * chunk;
     const float share = a.norm ? 1.f / a.d : 1.f;
+
+    // the loading side: head lh of token lt
+    long long lt = t0;
+    int lh = 0;
+    const T* x = (const T*)s.x + (on ? lt * s.stride_t + h0 * s.stride_h : 0) + c;
+    const T* dy = (const T*)s.dy + (on ? (lt * s.H + h0) * a.d : 0) + c;
+    const long long next_x = stride * s.stride_t - chunk * s.stride_h, next_dy = ((long long)stride * s.H - chunk) * a.d;
+    auto load = [&](int stage) {  // heads past the end become zeros
+        const bool fill = lh < heads && lt < a.n;
+        uint4* to = ring + (size_t)stage * 2 * W * kThreads + threadIdx.x;
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            cp_async16(to + i * kThreads, fill ? (const void*)(x + i * 16 / sizeof(T)) : s.x, fill);
+            cp_async16(to + (W + i) * kThreads, fill ? (const void*)(dy + i * 16 / sizeof(T)) : s.dy, fill);
+        }
+        cp_async_commit();
+        x += s.stride_h;
+        dy += a.d;
+        if (++lh == chunk) {
+            lh = 0;
+            lt += stride;
+            x += next_x;
+            dy += next_dy;
+        }
+    };
+#pragma unroll 1
+    for (int i = 0; i < S - 1; ++i) load(i);
     Raw<T> w;
     w.clear();
     if (s.w && on) w.load((const T*)s.w + c);
-    float dw[8] = {};
-    // the bound is the same for all groups of a CTA: the shuffles take whole warps
-    for (long long base = (long long)cta * GROUPS; base < items; base += (long long)ctas * GROUPS) {
-        const long long item = base + threadIdx.x / LANES;
-        const bool live = item < items, mine = live && on;
-        const long long t = live ? item / chunks : 0;
-        const int h0 = (int)(item % chunks) * chunk, heads = live ? min(chunk, s.H - h0) : 0;
-        const T* x = (const T*)s.x + t * s.stride_t + (live ? h0 * s.stride_h : 0) + c;
-        const long long out = (live ? (t * s.H + h0) * a.d : 0) + c;
-        const T* dy = (const T*)s.dy + out;
-        T* dx = (T*)s.y + out;
-        Raw<T> vx, vy;
-        vx.clear();
-        vy.clear();
-        if (mine && heads > 0) {
-            vx.load(x);
-            vy.load(dy);
-        }
-        float cs[8], sn[8];
-        int from = lane;
-        if (mine) from = turn_of<MODE>(a, t, c, lane, cs, sn);
-        else {
+    F2 dw[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) cs[e] = sn[e] = 0.f;
-        }
-        const int rounds = __reduce_max_sync(~0u, heads);
-        for (int h = 0; h < rounds; ++h) {
-            const Raw<T> ux = vx, uy = vy;
-            if (mine && h + 1 < heads) {
-                vx.load(x + (h + 1) * s.stride_h);
-                vy.load(dy + (long long)(h + 1) * a.d);
+    for (int e = 0; e < 4; ++e) dw[e] = f2(0.f, 0.f);
+
+    long long t = t0 - (long long)stride, pos = 0;
+    auto ahead = [&](long long at) { return MODE != kNoTurn && on && at < a.n ? position_of(a, at) : 0; };
+    pos = ahead(t0);
+    T* dx = (T*)s.y + (on ? (t * s.H + h0) * a.d : 0) + c;
+    F2 cs[4], sn[4];
+    int from = lane, h = chunk, stage = 0, into = S - 1;  // h: so that the first step begins a token
+    bool mine = false;
+#pragma unroll 1
+    for (long long step = 0; step < steps; ++step) {
+        if (h == chunk) {
+            h = 0;
+            t += stride;
+            dx += (long long)stride * s.H * a.d;
+            mine = on && t < a.n;
+            float cc[8], ss[8];
+            from = lane;
+            if (mine) from = turn_of<MODE>(a, pos, c, lane, cc, ss);
+            else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) cc[e] = ss[e] = 0.f;
             }
-            const bool do_it = mine && h < heads;
-            const Raw<T> p = partners<T, MODE>(uy, from);
-            float u[8], ss = 0.f, dot = 0.f;
+            pos = ahead(t + stride);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {  // u = R^T dy: the same cosine, the sine with the other sign
-                u[e] = uy.get(e) * cs[e];
-                if (MODE != kNoTurn) u[e] = fmaf(p.get(e), -sn[e], u[e]);
-                u[e] *= s.scale;
-                ss = fmaf(ux.get(e), ux.get(e), ss);
+            for (int e = 0; e < 4; ++e) {
+                cs[e] = f2(cc[2 * e] * s.scale, cc[2 * e + 1] * s.scale);
+                sn[e] = f2(-ss[2 * e] * s.scale, -ss[2 * e + 1] * s.scale);  // R^T: the sine with the other sign
             }
-            ss = group_sum<LANES>(ss);
-            const float r = rnorm<T, LANES>(ux, ss, share, a.eps);
-            float n[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                n[e] = ux.get(e) * r;
-                if (do_it) dw[e] = fmaf(u[e], n[e], dw[e]);
-                if (s.w) u[e] *= w.get(e);
-                dot = fmaf(u[e], n[e], dot);
-            }
-            dot = group_sum<LANES>(dot) * share;
-            float o[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = r * fmaf(-n[e], dot, u[e]);
-            if (do_it) store8(dx + (long long)h * a.d, o);
         }
+        cp_async_wait<S - 2>();
+        Raw<T> ux, uy;
+        ux.load_pieces(ring + (size_t)stage * 2 * W * kThreads + threadIdx.x, kThreads);
+        uy.load_pieces(ring + (size_t)(stage * 2 + 1) * W * kThreads + threadIdx.x, kThreads);
+        load(into);
+        into = into + 1 == S ? 0 : into + 1;
+        stage = stage + 1 == S ? 0 : stage + 1;
+        const Raw<T> p = partners<T, MODE>(uy, from);
+        F2 u[4], sum = f2(0.f, 0.f), dot = f2(0.f, 0.f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            u[e] = f2_mul(uy.pair(e), cs[e]);
+            if (MODE != kNoTurn) u[e] = f2_fma(p.pair(e), sn[e], u[e]);
+            sum = f2_fma(ux.pair(e), ux.pair(e), sum);
+        }
+        const float2 sums = f2_parts(sum);
+        const float r = rnorm<T, LANES>(ux, group_sum<LANES>(sums.x + sums.y), share, a.eps);
+        const F2 r2 = f2(r, r);
+        F2 n[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {  // heads past the end are zeros: they add none to dw
+            n[e] = f2_mul(ux.pair(e), r2);
+            dw[e] = f2_fma(u[e], n[e], dw[e]);
+            if (s.w) u[e] = f2_mul(u[e], w.pair(e));
+            dot = f2_fma(u[e], n[e], dot);
+        }
+        const float2 dots = f2_parts(dot);
+        const float m = -share * group_sum<LANES>(dots.x + dots.y);
+        const F2 m2 = f2(m, m);
+        float o[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 y = f2_parts(f2_mul(r2, f2_fma(n[e], m2, u[e])));
+            o[2 * e] = y.x;
+            o[2 * e + 1] = y.y;
+        }
+        if (mine && h < heads) store8(dx + (long long)h * a.d, o);
+        ++h;
     }
-    if (!part) return;
+    cp_async_wait<0>();
+    if (!part_sums) return;
+    __shared__ float s_dw[kThreads / 32][LANES * 8];
     // groups of the warp, then warps, then (qk_dw_kernel) CTAs
+    float all[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float2 y = f2_parts(dw[e]);
+        all[2 * e] = y.x;
+        all[2 * e + 1] = y.y;
+    }
 #pragma unroll
     for (int e = 0; e < 8; ++e)
 #pragma unroll
-        for (int o = LANES; o < 32; o <<= 1) dw[e] += __shfl_xor_sync(~0u, dw[e], o);
+        for (int o = LANES; o < 32; o <<= 1) all[e] += __shfl_xor_sync(~0u, all[e], o);
     if (lane < LANES) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s_dw[threadIdx.x / 32][c + e] = dw[e];
+        for (int e = 0; e < 8; ++e) s_dw[threadIdx.x / 32][c + e] = all[e];
     }
     __syncthreads();
     for (int i = threadIdx.x; i < a.d; i += kThreads) {
         float sum = 0.f;
 #pragma unroll
         for (int k = 0; k < kThreads / 32; ++k) sum += s_dw[k][i];
-        part[(size_t)blockIdx.x * a.d + i] = sum;
+        part_sums[(size_t)blockIdx.x * a.d + i] = sum;
     }
 }
 
@@ -340,7 +411,7 @@ __global__ void __launch_bounds__(1024) qk_dw_kernel(const float* part, float* d
     if (x == 0 && blockIdx.y * 32 + y < d) dw[blockIdx.y * 32 + y] = sum;
 }
 
-constexpr int kBwdCtas = 592;
+constexpr long long kBwdCtas = 296;  // two on each of 148 SMs
 
 template <typename F> cudaError_t with_lanes(int d, F f) {
     if (d <= 8) return f(std::integral_constant<int, 1>());
@@ -385,20 +456,30 @@ cudaError_t launch_qk_norm_rope_bwd(const QkArgs& a, cudaStream_t stream) {
     const cudaError_t err = with_lanes(a.d, [&](auto lanes) {
         return with_mode(a, [&](auto mode) {
             constexpr int L = decltype(lanes)::value, M = decltype(mode)::value, GROUPS = kThreads / L;
-            int chunk = 4;
-            auto items = [&](int H) { return (long long)a.n * ((H + chunk - 1) / chunk); };
-            while (chunk > 1 && (items(a.Hq) + items(a.Hk)) * L < 148ll * 1024) chunk /= 2;
-            // CTAs of each side in the ratio of their heads, no more than there is work for
-
-            const int all = a.Hq + a.Hk;
-            q_ctas = all ? (int)std::min((long long)(kBwdCtas - 1) * a.Hq / all + (a.Hq > 0), (items(a.Hq) + GROUPS - 1) / GROUPS) : 0;
-
-            const int k_ctas = (int)std::min((long long)(kBwdCtas - q_ctas), (items(a.Hk) + GROUPS - 1) / GROUPS);
+            // Heads of a group: up to 8, in equal parts; fewer where there are few tokens, more where there are so many
+            // heads that their parts would outnumber the groups.
+            int most = std::max(8, (a.Hq + a.Hk + 63) / 64);
+            auto parts_of = [&](int H) { return (H + most - 1) / most; };
+            auto parts = [&] { return (long long)parts_of(a.Hq) + parts_of(a.Hk); };
+            while (most > 1 && a.n * parts() * L < 148ll * 512 && 2 * parts() + 2 <= 148 * GROUPS) most /= 2;
+            auto chunk_of = [&](int H) { return H ? (H + parts_of(H) - 1) / parts_of(H) : 1; };
+            // CTAs of each side in the ratio of its work: groups for every part at least, for every part of a token at most
+            auto fewest = [&](int H) { return ((long long)parts_of(H) + GROUPS - 1) / GROUPS; };
+            auto useful = [&](int H) { return ((long long)a.n * parts_of(H) + GROUPS - 1) / GROUPS; };
+            const long long q_work = (long long)parts_of(a.Hq) * chunk_of(a.Hq), work = q_work + (long long)parts_of(a.Hk) * chunk_of(a.Hk);
+            if (a.n == 0 || work == 0) return cudaSuccess;
+            const long long q = std::min(std::max(kBwdCtas * q_work / work, fewest(a.Hq)), kBwdCtas - fewest(a.Hk));
+            q_ctas = (int)std::min(q, useful(a.Hq));
+            const int k_ctas = (int)std::min(kBwdCtas - q_ctas, useful(a.Hk));
             ctas = q_ctas + k_ctas;
-            if (ctas == 0) return cudaSuccess;
-            if (a.bf16) qk_bwd_kernel<__nv_bfloat16, L, M><<<ctas, kThreads, 0, stream>>>(a, chunk, q_ctas, part);
-            else qk_bwd_kernel<float, L, M><<<ctas, kThreads, 0, stream>>>(a, chunk, q_ctas, part);
-            return cudaGetLastError();
+            auto go = [&](auto kernel, int smem) {
+                const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+                if (e != cudaSuccess) return e;
+                kernel<<<ctas, kThreads, smem, stream>>>(a, chunk_of(a.Hq), chunk_of(a.Hk), q_ctas, part);
+                return cudaGetLastError();
+            };
+            if (a.bf16) return go(qk_bwd_kernel<__nv_bfloat16, L, M>, BwdPlan<__nv_bfloat16>::kSmem);
+            return go(qk_bwd_kernel<float, L, M>, BwdPlan<float>::kSmem);
         });
     });
     if (err != cudaSuccess || !part) return err;
