@@ -65,6 +65,18 @@ template <typename T> struct Raw {
         if constexpr (W == 8) return __uint_as_float(w[i]);
         else return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
     }
+    // By a power of two: exact but for what falls below the type's smallest numbers.
+    __device__ __forceinline__ void scale(float f) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            if constexpr (W == 8) {
+                w[i] = __float_as_uint(get(i) * f);
+            } else {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(get(2 * i) * f, get(2 * i + 1) * f);
+                w[i] = *reinterpret_cast<const uint32_t*>(&b);
+            }
+        }
+    }
     __device__ __forceinline__ F2 pair(int i) const { return f2(get(2 * i), get(2 * i + 1)); }
 };
 
@@ -85,6 +97,16 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&y)[8]) {
 template <int LANES> __device__ __forceinline__ float group_sum(float x) {
 #pragma unroll
     for (int o = LANES / 2; o > 0; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+    return x;
+}
+
+// Two sums at once.
+template <int LANES> __device__ __forceinline__ F2 group_sum2(F2 x) {
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) {
+        const float2 p = f2_parts(x);
+        x = f2_add(x, f2(__shfl_xor_sync(~0u, p.x, o), __shfl_xor_sync(~0u, p.y, o)));
+    }
     return x;
 }
 
@@ -263,7 +285,6 @@ __global__ void __launch_bounds__(kThreads, 2) qk_bwd_kernel(QkArgs a, int q_chu
     const bool on = c < a.d && t0 < stride;
     const int heads = on ? min(chunk, s.H - h0) : 0;
     const int rounds = (int)(((long long)a.n + stride - 1) / stride);  // the same for all groups: the shuffles take whole warps
-    const long long steps = (long long)rounds * chunk;
     const float share = a.norm ? 1.f / a.d : 1.f;
 
     // the loading side: head lh of token lt
@@ -273,12 +294,12 @@ __global__ void __launch_bounds__(kThreads, 2) qk_bwd_kernel(QkArgs a, int q_chu
     const T* dy = (const T*)s.dy + (on ? (lt * s.H + h0) * a.d : 0) + c;
     const long long next_x = stride * s.stride_t - chunk * s.stride_h, next_dy = ((long long)stride * s.H - chunk) * a.d;
     auto load = [&](int stage) {  // heads past the end become zeros
-        const bool fill = lh < heads && lt < a.n;
-        uint4* to = ring + (size_t)stage * 2 * W * kThreads + threadIdx.x;
+        const bool fill = lh < heads && lt < a.n;  // a copy of zeros does not touch its source
+        uint4* to = ring + stage * 2 * W * kThreads + threadIdx.x;
 #pragma unroll
         for (int i = 0; i < W; ++i) {
-            cp_async16(to + i * kThreads, fill ? (const void*)(x + i * 16 / sizeof(T)) : s.x, fill);
-            cp_async16(to + (W + i) * kThreads, fill ? (const void*)(dy + i * 16 / sizeof(T)) : s.dy, fill);
+            cp_async16(to + i * kThreads, x + i * 16 / sizeof(T), fill);
+            cp_async16(to + (W + i) * kThreads, dy + i * 16 / sizeof(T), fill);
         }
         cp_async_commit();
         x += s.stride_h;
@@ -292,79 +313,94 @@ __global__ void __launch_bounds__(kThreads, 2) qk_bwd_kernel(QkArgs a, int q_chu
     };
 #pragma unroll 1
     for (int i = 0; i < S - 1; ++i) load(i);
-    Raw<T> w;
-    w.clear();
-    if (s.w && on) w.load((const T*)s.w + c);
-    F2 dw[4];
+    F2 w[4], dw[4];
+    {
+        Raw<T> raw;
+        raw.clear();
+        if (s.w && on) raw.load((const T*)s.w + c);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) dw[e] = f2(0.f, 0.f);
-
-    long long t = t0 - (long long)stride, pos = 0;
+        for (int e = 0; e < 4; ++e) {
+            w[e] = s.w ? raw.pair(e) : f2(1.f, 1.f);
+            dw[e] = f2(0.f, 0.f);
+        }
+    }
     auto ahead = [&](long long at) { return MODE != kNoTurn && on && at < a.n ? position_of(a, at) : 0; };
-    pos = ahead(t0);
+    long long t = t0, pos = ahead(t0);
     T* dx = (T*)s.y + (on ? (t * s.H + h0) * a.d : 0) + c;
-    F2 cs[4], sn[4];
-    int from = lane, h = chunk, stage = 0, into = S - 1;  // h: so that the first step begins a token
-    bool mine = false;
+    const long long next_dx = ((long long)stride * s.H - chunk) * a.d;
+    int stage = 0, into = S - 1;
 #pragma unroll 1
-    for (long long step = 0; step < steps; ++step) {
-        if (h == chunk) {
-            h = 0;
-            t += stride;
-            dx += (long long)stride * s.H * a.d;
-            mine = on && t < a.n;
-            float cc[8], ss[8];
-            from = lane;
-            if (mine) from = turn_of<MODE>(a, pos, c, lane, cc, ss);
-            else {
+    for (int round = 0; round < rounds; ++round, t += stride, dx += next_dx) {
+        const int mine = t < a.n ? heads : 0;  // heads of this token
+        float cc[8], ss[8];
+        int from = lane;
+        if (mine) from = turn_of<MODE>(a, pos, c, lane, cc, ss);
+        else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) cc[e] = ss[e] = 0.f;
-            }
-            pos = ahead(t + stride);
+            for (int e = 0; e < 8; ++e) cc[e] = ss[e] = 0.f;
+        }
+        pos = ahead(t + stride);
+        F2 cs[4], sn[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            cs[e] = f2(cc[2 * e] * s.scale, cc[2 * e + 1] * s.scale);
+            sn[e] = f2(-ss[2 * e] * s.scale, -ss[2 * e + 1] * s.scale);  // R^T: the sine with the other sign
+        }
+#pragma unroll 1
+        for (int h = 0; h < chunk; ++h, dx += a.d) {
+            cp_async_wait<S - 2>();
+            Raw<T> ux, uy;
+            ux.load_pieces(ring + stage * 2 * W * kThreads + threadIdx.x, kThreads);
+            uy.load_pieces(ring + (stage * 2 + 1) * W * kThreads + threadIdx.x, kThreads);
+            load(into);
+            into = stage;
+            stage = stage + 1 == S ? 0 : stage + 1;
+            const Raw<T> p = partners<T, MODE>(uy, from);
+            F2 u[4], uw[4], sum = f2(0.f, 0.f), dot = f2(0.f, 0.f);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                cs[e] = f2(cc[2 * e] * s.scale, cc[2 * e + 1] * s.scale);
-                sn[e] = f2(-ss[2 * e] * s.scale, -ss[2 * e + 1] * s.scale);  // R^T: the sine with the other sign
+                u[e] = f2_mul(uy.pair(e), cs[e]);
+                if (MODE != kNoTurn) u[e] = f2_fma(p.pair(e), sn[e], u[e]);
+                uw[e] = f2_mul(u[e], w[e]);
+                sum = f2_fma(ux.pair(e), ux.pair(e), sum);
+                dot = f2_fma(uw[e], ux.pair(e), dot);  // of x: of n it is r times that
             }
-        }
-        cp_async_wait<S - 2>();
-        Raw<T> ux, uy;
-        ux.load_pieces(ring + (size_t)stage * 2 * W * kThreads + threadIdx.x, kThreads);
-        uy.load_pieces(ring + (size_t)(stage * 2 + 1) * W * kThreads + threadIdx.x, kThreads);
-        load(into);
-        into = into + 1 == S ? 0 : into + 1;
-        stage = stage + 1 == S ? 0 : stage + 1;
-        const Raw<T> p = partners<T, MODE>(uy, from);
-        F2 u[4], sum = f2(0.f, 0.f), dot = f2(0.f, 0.f);
+            const float2 sums = f2_parts(sum), dots = f2_parts(dot);
+            F2 both = group_sum2<LANES>(f2(sums.x + sums.y, dots.x + dots.y));
+            float2 all = f2_parts(both);
+            float r = rsqrtf(fmaf(all.x, share, a.eps)), r_out = r;
+            const bool out = !(all.x < 1e37f);
+            if (__any_sync(~0u, out)) {  // squares that leave 32 bits: the same from 2^-80 x, exact in T
+                Raw<T> small = ux;
+                small.scale(0x1p-80f);
+                sum = dot = f2(0.f, 0.f);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            u[e] = f2_mul(uy.pair(e), cs[e]);
-            if (MODE != kNoTurn) u[e] = f2_fma(p.pair(e), sn[e], u[e]);
-            sum = f2_fma(ux.pair(e), ux.pair(e), sum);
-        }
-        const float2 sums = f2_parts(sum);
-        const float r = rnorm<T, LANES>(ux, group_sum<LANES>(sums.x + sums.y), share, a.eps);
-        const F2 r2 = f2(r, r);
-        F2 n[4];
+                for (int e = 0; e < 4; ++e) {
+                    sum = f2_fma(small.pair(e), small.pair(e), sum);
+                    dot = f2_fma(uw[e], small.pair(e), dot);
+                }
+                const float2 s2 = f2_parts(sum), d2 = f2_parts(dot);
+                const float2 again = f2_parts(group_sum2<LANES>(f2(s2.x + s2.y, d2.x + d2.y)));
+                if (out) {
+                    ux = small;
+                    all.y = again.y;
+                    r = rsqrtf(again.x * share);
+                    r_out = 0x1p-80f * r;
+                }
+            }
+            const float m = -share * r * all.y;
+            const F2 r2 = f2(r, r), m2 = f2(m, m), ro = f2(r_out, r_out);
+            float o[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {  // heads past the end are zeros: they add none to dw
-            n[e] = f2_mul(ux.pair(e), r2);
-            dw[e] = f2_fma(u[e], n[e], dw[e]);
-            if (s.w) u[e] = f2_mul(u[e], w.pair(e));
-            dot = f2_fma(u[e], n[e], dot);
+            for (int e = 0; e < 4; ++e) {  // heads past the end are zeros: they add none to dw
+                const F2 n = f2_mul(ux.pair(e), r2);
+                dw[e] = f2_fma(u[e], n, dw[e]);
+                const float2 y = f2_parts(f2_mul(ro, f2_fma(n, m2, uw[e])));
+                o[2 * e] = y.x;
+                o[2 * e + 1] = y.y;
+            }
+            if (h < mine) store8(dx, o);
         }
-        const float2 dots = f2_parts(dot);
-        const float m = -share * group_sum<LANES>(dots.x + dots.y);
-        const F2 m2 = f2(m, m);
-        float o[8];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float2 y = f2_parts(f2_mul(r2, f2_fma(n[e], m2, u[e])));
-            o[2 * e] = y.x;
-            o[2 * e + 1] = y.y;
-        }
-        if (mine && h < heads) store8(dx + (long long)h * a.d, o);
-        ++h;
     }
     cp_async_wait<0>();
     if (!part_sums) return;
