@@ -10,16 +10,18 @@
 //
 // What bounds it: HBM, 3 (backward 5) elements of the tensors per token and
 // channel, each read or written once. One cluster of CTAs owns a (sequence,
-// slice of 128 bytes of channels) and walks the tokens; each pass of the walk is
-// a tile of tokens per CTA, held in registers: a thread has R consecutive tokens
-// of 16 bytes of channels, composes them, the four token groups of a warp are
-// composed by shuffles, the warps through shared memory, the CTAs of the cluster
-// through distributed shared memory (one cluster barrier a tile), and the thread
-// then runs its tokens again from the state that enters them. The next tile's
-// loads are in flight meanwhile. The sequential depth is T / (tokens of a
-// cluster's tile); clusters of more than one CTA are taken where sequences times
-// channel slices do not fill the GPU. Nothing waits on a flag, and the order of
-// every product and sum is fixed by the sizes alone.
+// slice of 128 bytes of channels) and walks the tokens, a tile of tokens per CTA
+// at a time. A thread has R consecutive tokens of 16 bytes of channels; it copies
+// them into shared memory two tiles ahead (it alone reads them back, so no
+// barrier is due) and then
+//   1. composes its tokens into one span (A, H) and leaves it in shared memory;
+//   2. as (channel, part) composes the spans of one part of the CTA's token
+//      groups, and hands the part's span to every CTA of the cluster;
+//   3. walks the parts before its own, which gives the state that enters each of
+//      its groups, and leaves these in shared memory;
+//   4. runs its tokens again from the state that enters them and writes them.
+// The sequential depth is T / (tokens of a cluster's tile). Nothing waits on a
+// flag, and the order of every product and sum is fixed by the sizes alone.
 #include "kda_common.cuh"
 #include "kda_internal.h"
 
@@ -31,7 +33,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 256;
 constexpr int kGroups = kThreads / 8;  // token groups of a CTA (8 threads across the channels)
 constexpr int kMaxCluster = 8;
 
@@ -56,83 +58,117 @@ template <typename T> struct Pack {
         if constexpr (V == 4) return __uint_as_float(w[i]);
         else return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
     }
-    __device__ __forceinline__ void clear() { w[0] = w[1] = w[2] = w[3] = 0u; }
+    static __device__ __forceinline__ Pack of(const uint4& v) {
+        Pack p;
+        p.w[0] = v.x; p.w[1] = v.y; p.w[2] = v.z; p.w[3] = v.w;
+        return p;
+    }
 };
 
-template <typename T> __device__ __forceinline__ float decay(float log_alpha);
+// e^x. For bf16 inputs 2^(x log2 e), off by 2^-22 for |x| < 1: far below the input's own step.
+template <typename T> __device__ __forceinline__ float decay(float x);
 template <> __device__ __forceinline__ float decay<float>(float x) { return expf(x); }
-// two units in the last place of 32 bits off at most for |x| < 1: far below a bf16 input's own step
-template <> __device__ __forceinline__ float decay<__nv_bfloat16>(float x) { return __expf(x); }
-
-// Channel i of this thread, within the slice: neighbours where 16-byte rows allow
-// wide accesses; else eight apart, so that the eight threads of a token group
-// read neighbouring elements.
-template <typename T, bool ALIGNED> __device__ __forceinline__ int channel_of(int col, int i) {
-    return ALIGNED ? col * Pack<T>::V + i : col + 8 * i;
+template <> __device__ __forceinline__ float decay<__nv_bfloat16>(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+    return y;
 }
 
-template <typename T, bool ALIGNED>
-__device__ __forceinline__ Pack<T> load_row(const T* row, int c0, int col, int D, bool on) {
-    constexpr int V = Pack<T>::V;
-    Pack<T> p;
-    p.clear();
-    if (!on) return p;
-    if constexpr (ALIGNED) {
-        if (c0 + col * V < D) {
-            const uint4 v = __ldcs(reinterpret_cast<const uint4*>(row + c0 + col * V));
-            p.w[0] = v.x; p.w[1] = v.y; p.w[2] = v.z; p.w[3] = v.w;
-        }
-    } else if constexpr (V == 4) {
+// ALIGN: what every row's first byte is a multiple of, 16, 4 or (bf16 alone) 2. It sets a thread's channels within the
+// slice: 16 bytes at once; else 4-byte words eight apart, so that the eight threads of a token group touch neighbouring
+// words; else single elements eight apart.
+template <typename T, int ALIGN> __device__ __forceinline__ int channel_of(int col, int e) {
+    constexpr int V = Pack<T>::V, P = 4 / sizeof(T);  // elements of a word
+    if (ALIGN == 16) return col * V + e;
+    if (ALIGN == 4) return (col + 8 * (e / P)) * P + e % P;
+    return col + 8 * e;
+}
+
+__device__ __forceinline__ void cp_async4(void* dst, const void* src, bool on) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+                 "l"(src), "r"(on ? 4 : 0)
+                 : "memory");
+}
+
+// One row's channels of this thread into its 16 bytes at `to`; zeros where `on` is false or past the last channel.
+template <typename T, int ALIGN>
+__device__ __forceinline__ void copy_row(uint4* to, const T* row, int c0, int col, int D, bool on) {
+    constexpr int P = 4 / sizeof(T);
+    if constexpr (ALIGN == 16) {
+        const int c = c0 + col * Pack<T>::V;
+        cp_async16(to, row + c, on && c < D);
+    } else if constexpr (ALIGN == 4) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int c = c0 + channel_of<T, false>(col, i);
-            if (c < D) p.w[i] = __float_as_uint(__ldcs(reinterpret_cast<const float*>(row) + c));
+        for (int j = 0; j < 4; ++j) {
+            const int c = c0 + (col + 8 * j) * P;
+            cp_async4(reinterpret_cast<uint32_t*>(to) + j, row + c, on && c < D);
         }
     } else {
+        uint32_t w[4] = {};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int c = c0 + channel_of<T, false>(col, i);
-            if (c < D) p.w[i >> 1] |= (uint32_t)__ldcs(reinterpret_cast<const unsigned short*>(row) + c) << (i & 1 ? 16 : 0);
+        for (int e = 0; e < 8; ++e) {
+            const int c = c0 + col + 8 * e;
+            if (on && c < D) w[e >> 1] |= (uint32_t)reinterpret_cast<const unsigned short*>(row)[c] << (e & 1 ? 16 : 0);
         }
+        *to = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    return p;
 }
 
-template <typename T, bool ALIGNED>
+template <typename T, int ALIGN>
 __device__ __forceinline__ void store_row(T* row, int c0, int col, int D, const float (&x)[Pack<T>::V]) {
-    constexpr int V = Pack<T>::V;
-    if constexpr (ALIGNED) {
-        if (c0 + col * V >= D) return;
-        uint4 v;
-        if constexpr (V == 4) {
-            v = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
-        } else {
-            uint32_t w[4];
+    constexpr int V = Pack<T>::V, P = 4 / sizeof(T);
+    if constexpr (ALIGN == 2) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+        for (int e = 0; e < V; ++e) {
+            const int c = c0 + channel_of<T, ALIGN>(col, e);
+            if (c < D) row[c] = from_f32<T>(x[e]);
+        }
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (V == 4) {
+                w[i] = __float_as_uint(x[i]);
+            } else {
                 const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
                 w[i] = *reinterpret_cast<const uint32_t*>(&b);
             }
-            v = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        __stcs(reinterpret_cast<uint4*>(row + c0 + col * V), v);
-    } else {
+        if constexpr (ALIGN == 16) {
+            if (c0 + col * V < D) __stcs(reinterpret_cast<uint4*>(row + c0 + col * V), make_uint4(w[0], w[1], w[2], w[3]));
+        } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int c = c0 + channel_of<T, false>(col, i);
-            if (c < D) row[c] = from_f32<T>(x[i]);
+            for (int j = 0; j < 4; ++j) {
+                const int c = c0 + (col + 8 * j) * P;
+                if (c < D) *reinterpret_cast<uint32_t*>(row + c) = w[j];
+            }
         }
     }
 }
 
+// Shared memory: the ring of stages, the spans of the token groups, the states that enter them, and the spans of the
+// parts of all CTAs of the cluster, by parity of the tile.
+template <typename T, bool BWD, int R> struct ScanSmem {
+    static constexpr int CT = 8 * Pack<T>::V;              // channels of a slice
+    static constexpr int kParts = kThreads / CT, kPer = kGroups / kParts;
+    static constexpr int kStreams = BWD ? 3 : 2;
+    static constexpr int kStage = kStreams * R * kThreads * 16, kStages = 2;
+    static constexpr int kSpans = kGroups * CT * (int)sizeof(float2), kStates = kGroups * CT * (int)sizeof(float);
+    static constexpr int kRank = kParts * CT * (int)sizeof(float2);
+    static constexpr int bytes(int size) { return kStages * kStage + kSpans + kStates + 2 * size * kRank; }
+};
+
 // R: tokens of a thread. CLUSTER: the cluster has more than one CTA.
-template <typename T, bool ALIGNED, bool BWD, int R, bool CLUSTER>
+template <typename T, int ALIGN, bool BWD, int R, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads, 2) recurrence_scan_kernel(RecurrenceArgs a, int slices) {
-    constexpr int V = Pack<T>::V, CT = 8 * V, TILE = kGroups * R;
-    __shared__ float2 s_warp[kWarps][CT];                               // a warp's span, then what enters it from the CTA's start
-    __shared__ float2 s_cta[CLUSTER ? 2 : 1][CLUSTER ? kMaxCluster : 1][CT];  // the CTAs' spans, by parity of the tile
-    __shared__ float s_in[CT];                                          // the state that enters this CTA's tile
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, col = lane & 7, group = tid >> 3;
+    using Sm = ScanSmem<T, BWD, R>;
+    constexpr int V = Pack<T>::V, CT = Sm::CT, TILE = kGroups * R, PARTS = Sm::kParts, PER = Sm::kPer, S = Sm::kStages;
+    extern __shared__ __align__(16) unsigned char smem[];
+    uint4* ring = reinterpret_cast<uint4*>(smem);
+    float4* spans = reinterpret_cast<float4*>(smem + S * Sm::kStage);                  // [group][pair of V/2][col]: A, H, A, H
+    float* states = reinterpret_cast<float*>(smem + S * Sm::kStage + Sm::kSpans);      // [group][quad of V/4][col][4]
+    float2* ranks = reinterpret_cast<float2*>(smem + S * Sm::kStage + Sm::kSpans + Sm::kStates);  // [parity][rank][part][channel]
+    const int tid = threadIdx.x, col = tid & 7, group = tid >> 3;
     int rank = 0, size = 1;
     long long id = blockIdx.x;
     if constexpr (CLUSTER) {
@@ -150,9 +186,11 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_scan_kernel(Recurrence
     T* out = (T*)a.out + begin * D;
     T* out_la = BWD ? (T*)a.out_la + begin * D : nullptr;
 
-    // Threads tid < CT keep the state of channel c0 + tid between tiles.
-    const bool keeps = tid < CT && c0 + tid < D;
-    float state = keeps && a.state0 ? a.state0[(long long)n * D + c0 + tid] : 0.f;
+    // As (channel, part): channel p in the order of `spans`, that is element e = 2 pair + half of thread column pcol. Every
+    // part keeps the channel's state, by the same operations.
+    const int p = tid % CT, part = tid / CT, pair = p / 16, pcol = p % 16 / 2, half = p % 2;
+    const int pc = c0 + channel_of<T, ALIGN>(pcol, 2 * pair + half);
+    float state = pc < D && a.state0 ? a.state0[(long long)n * D + pc] : 0.f;
     if constexpr (CLUSTER) cg::this_cluster().sync();  // every CTA has started, and has read its state
 
     // token of this thread's step i in tile `tile`, in walking order; -1: past the end
@@ -160,134 +198,134 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_scan_kernel(Recurrence
         const unsigned at = (unsigned)(tile * size + rank) * TILE + group * R + i;  // below len + 8 TILE: no wrap
         return at < (unsigned)len ? (BWD ? len - 1 - (int)at : (int)at) : -1;
     };
-    Pack<T> pl[R], px[R], ph[BWD ? R : 1];
     auto fetch = [&](int tile) {
+        uint4* to = ring + (size_t)(tile & 1) * (Sm::kStage / 16) + tid;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             const int t = token(tile, i);
             const long long row = (long long)max(t, 0) * D;
-            pl[i] = load_row<T, ALIGNED>(la + row, c0, col, D, t >= 0);
-            px[i] = load_row<T, ALIGNED>(x + row, c0, col, D, t >= 0);
-            if constexpr (BWD) ph[i] = load_row<T, ALIGNED>(hf + row - (t > 0 ? D : 0), c0, col, D, t > 0);
+            copy_row<T, ALIGN>(to + (i * Sm::kStreams) * kThreads, la + row, c0, col, D, t >= 0);
+            copy_row<T, ALIGN>(to + (i * Sm::kStreams + 1) * kThreads, x + row, c0, col, D, t >= 0);
+            if constexpr (BWD)  // h_{t-1}
+                copy_row<T, ALIGN>(to + (i * Sm::kStreams + 2) * kThreads, hf + row - (t > 0 ? D : 0), c0, col, D, t > 0);
         }
     };
     const long long step = (long long)size * TILE;
     const int tiles = (int)((len + step - 1) / step);
-    if (tiles > 0) fetch(0);
+    for (int k = 0; k < S; ++k) {
+        if (k < tiles) fetch(k);
+        cp_async_commit();
+    }
     for (int tile = 0; tile < tiles; ++tile) {
-        Pack<T> cl[R], cx[R], ch[BWD ? R : 1];
+        // 1. this thread's tokens as one span
+        cp_async_wait<S - 1>();
+        F2 d[R][V / 2], A[V / 2], H[V / 2];
+        Pack<T> px[R], ph[BWD ? R : 1];
+        {
+            const uint4* from = ring + (size_t)(tile & 1) * (Sm::kStage / 16) + tid;
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            cl[i] = pl[i];
-            cx[i] = px[i];
-            if constexpr (BWD) ch[i] = ph[i];
-        }
-        if (tile + 1 < tiles) fetch(tile + 1);
-        // this thread's tokens as one span
-        float A[V], H[V];
+            for (int i = 0; i < R; ++i) {
+                const Pack<T> pl = Pack<T>::of(from[(i * Sm::kStreams) * kThreads]);
+                px[i] = Pack<T>::of(from[(i * Sm::kStreams + 1) * kThreads]);
+                if constexpr (BWD) ph[i] = Pack<T>::of(from[(i * Sm::kStreams + 2) * kThreads]);
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            A[e] = 1.f;
-            H[e] = 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < R; ++i)
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float d = decay<T>(cl[i].get(e)), v = cx[i].get(e);
-                A[e] *= d;
-                H[e] = BWD ? d * (H[e] + v) : fmaf(d, H[e], v);
-            }
-        // composed over the warp's token groups (lanes 8 apart); E: what lies before this group in the warp
-        float EA[V], EH[V];
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            float pa = __shfl_up_sync(~0u, A[e], 8), pk = __shfl_up_sync(~0u, H[e], 8);
-            if (lane >= 8) {
-                H[e] = fmaf(A[e], pk, H[e]);
-                A[e] *= pa;
-            }
-            pa = __shfl_up_sync(~0u, A[e], 16);
-            pk = __shfl_up_sync(~0u, H[e], 16);
-            if (lane >= 16) {
-                H[e] = fmaf(A[e], pk, H[e]);
-                A[e] *= pa;
-            }
-            EA[e] = __shfl_up_sync(~0u, A[e], 8);
-            EH[e] = __shfl_up_sync(~0u, H[e], 8);
-            if (lane < 8) {
-                EA[e] = 1.f;
-                EH[e] = 0.f;
-            }
-            if (lane >= 24) s_warp[warp][channel_of<T, ALIGNED>(col, e)] = make_float2(A[e], H[e]);
-        }
-        __syncthreads();
-        if (tid < CT) {
-            float2 w[kWarps];
-#pragma unroll
-            for (int k = 0; k < kWarps; ++k) w[k] = s_warp[k][tid];
-            float2 all = make_float2(1.f, 0.f);
-#pragma unroll
-            for (int k = 0; k < kWarps; ++k) {
-                s_warp[k][tid] = all;
-                all = make_float2(all.x * w[k].x, fmaf(w[k].x, all.y, w[k].y));
-            }
-            if constexpr (CLUSTER) {
-                const cg::cluster_group cl_ = cg::this_cluster();
-                for (int r = 0; r < size; ++r)
-                    *cl_.map_shared_rank(&s_cta[tile & 1][rank][tid], r) = all;
-            } else {
-                s_in[tid] = state;
-                state = fmaf(all.x, state, all.y);
-            }
-        }
-        if constexpr (CLUSTER) {
-            cg::this_cluster().sync();
-            if (tid < CT) {
-                for (int r = 0; r < size; ++r) {
-                    if (r == rank) s_in[tid] = state;
-                    const float2 w = s_cta[tile & 1][r][tid];
-                    state = fmaf(w.x, state, w.y);
+                for (int e = 0; e < V / 2; ++e) {
+                    d[i][e] = f2(decay<T>(pl.get(2 * e)), decay<T>(pl.get(2 * e + 1)));
+                    const F2 v = f2(px[i].get(2 * e), px[i].get(2 * e + 1));
+                    if (i == 0) {
+                        A[e] = d[i][e];
+                        H[e] = BWD ? f2_mul(d[i][e], v) : v;
+                    } else {
+                        A[e] = f2_mul(A[e], d[i][e]);
+                        H[e] = BWD ? f2_mul(d[i][e], f2_add(H[e], v)) : f2_fma(d[i][e], H[e], v);
+                    }
                 }
             }
         }
-        __syncthreads();
-        // the tokens again, from the state that enters them
-        float s[V];
+        if (tile + S < tiles) fetch(tile + S);
+        cp_async_commit();
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            const int c = channel_of<T, ALIGNED>(col, e);
-            const float2 w = s_warp[warp][c];
-            s[e] = fmaf(EA[e], fmaf(w.x, s_in[c], w.y), EH[e]);
+        for (int e = 0; e < V / 2; ++e) {
+            const float2 A_ = f2_parts(A[e]), H_ = f2_parts(H[e]);
+            spans[(group * (V / 2) + e) * 8 + col] = make_float4(A_.x, H_.x, A_.y, H_.y);
+        }
+        __syncthreads();
+        // 2. as (channel, part): the part's span, to every CTA of the cluster
+        float2 w[PER];
+#pragma unroll
+        for (int k = 0; k < PER; ++k)
+            w[k] = reinterpret_cast<const float2*>(spans)[((part * PER + k) * (V / 2) + pair) * 16 + pcol * 2 + half];
+        float2 all = w[0];
+#pragma unroll
+        for (int k = 1; k < PER; ++k) all = make_float2(all.x * w[k].x, fmaf(w[k].x, all.y, w[k].y));
+        float2* mine = ranks + ((size_t)(tile & 1) * size + rank) * PARTS * CT + part * CT + p;
+        if constexpr (CLUSTER) {
+            const cg::cluster_group cl = cg::this_cluster();
+            for (int r = 0; r < size; ++r) *cl.map_shared_rank(mine, r) = all;
+            cl.sync();
+        } else {
+            *mine = all;
+            __syncthreads();
+        }
+        // 3. the state that enters this part's groups; the state after the cluster's tile
+        const float2* theirs = ranks + (size_t)(tile & 1) * size * PARTS * CT + p;
+        float s = 0.f;
+        for (int r = 0; r < size; ++r)
+#pragma unroll
+            for (int k = 0; k < PARTS; ++k) {
+                if (r == rank && k == part) s = state;
+                const float2 u = theirs[(r * PARTS + k) * CT];
+                state = fmaf(u.x, state, u.y);
+            }
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            states[(((part * PER + k) * (V / 4) + pair / 2) * 8 + pcol) * 4 + (pair & 1) * 2 + half] = s;
+            s = fmaf(w[k].x, s, w[k].y);
+        }
+        __syncthreads();
+        // 4. the tokens again, from the state that enters them
+        F2 cur[V / 2];
+#pragma unroll
+        for (int q = 0; q < V / 4; ++q) {
+            const float4 v = reinterpret_cast<const float4*>(states)[(group * (V / 4) + q) * 8 + col];
+            cur[2 * q] = f2(v.x, v.y);
+            cur[2 * q + 1] = f2(v.z, v.w);
         }
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             const int t = token(tile, i);
             float y[V], z[V];
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float d = decay<T>(cl[i].get(e)), v = cx[i].get(e);
+            for (int e = 0; e < V / 2; ++e) {
+                const F2 v = f2(px[i].get(2 * e), px[i].get(2 * e + 1));
+                F2 o;
                 if constexpr (BWD) {
-                    y[e] = s[e] + v;
-                    s[e] = d * y[e];
-                    float before = ch[i].get(e);
+                    o = f2_add(cur[e], v);
+                    cur[e] = f2_mul(d[i][e], o);
+                    float b0 = ph[i].get(2 * e), b1 = ph[i].get(2 * e + 1);
                     if (t == 0) {
-                        const int c = c0 + channel_of<T, ALIGNED>(col, e);
-                        before = a.h0 && c < D ? a.h0[(long long)n * D + c] : 0.f;
+                        const int e0 = c0 + channel_of<T, ALIGN>(col, 2 * e), e1 = c0 + channel_of<T, ALIGN>(col, 2 * e + 1);
+                        b0 = a.h0 && e0 < D ? a.h0[(long long)n * D + e0] : 0.f;
+                        b1 = a.h0 && e1 < D ? a.h0[(long long)n * D + e1] : 0.f;
                     }
-                    z[e] = s[e] * before;
+                    const float2 zz = f2_parts(f2_mul(cur[e], f2(b0, b1)));
+                    z[2 * e] = zz.x;
+                    z[2 * e + 1] = zz.y;
                 } else {
-                    y[e] = s[e] = fmaf(d, s[e], v);
+                    o = cur[e] = f2_fma(d[i][e], cur[e], v);
                 }
+                const float2 yy = f2_parts(o);
+                y[2 * e] = yy.x;
+                y[2 * e + 1] = yy.y;
             }
             if (t >= 0) {
-                store_row<T, ALIGNED>(out + (long long)t * D, c0, col, D, y);
-                if constexpr (BWD) store_row<T, ALIGNED>(out_la + (long long)t * D, c0, col, D, z);
+                store_row<T, ALIGN>(out + (long long)t * D, c0, col, D, y);
+                if constexpr (BWD) store_row<T, ALIGN>(out_la + (long long)t * D, c0, col, D, z);
             }
         }
-        __syncwarp();
     }
-    if (keeps && rank == 0 && a.state_end) a.state_end[(long long)n * D + c0 + tid] = state;
+    cp_async_wait<0>();
+    if (part == 0 && rank == 0 && pc < D && a.state_end) a.state_end[(long long)n * D + pc] = state;
 }
 
 template <typename T>
@@ -300,37 +338,42 @@ __global__ void recurrence_step_kernel(const T* log_alpha, const T* x, const flo
     y[i] = from_f32<T>(s);
 }
 
-template <typename T, bool ALIGNED, bool BWD>
+template <typename T, int ALIGN, bool BWD>
 cudaError_t launch_scan(const RecurrenceArgs& a, cudaStream_t stream) {
     constexpr int R = BWD ? 2 : 4;
-    const int slices = (a.D + 8 * Pack<T>::V - 1) / (8 * Pack<T>::V);
+    using Sm = ScanSmem<T, BWD, R>;
+    const int slices = (a.D + Sm::CT - 1) / Sm::CT;
     const long long rows = (long long)a.N * slices;
     // CTAs of a cluster: as many as fill two CTAs on each SM, no more than the tokens give tiles to
     const long long tokens = a.cu_seqlens ? (a.T + a.N - 1) / a.N : a.T;
     int size = 1;
     while (size < kMaxCluster && rows * size * 2 <= 2 * 148 && (long long)size * kGroups * R < tokens) size *= 2;
-    if (size == 1) {
-        recurrence_scan_kernel<T, ALIGNED, BWD, R, false><<<(unsigned)rows, kThreads, 0, stream>>>(a, slices);
-        return cudaGetLastError();
-    }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(rows * size));
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = size;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, recurrence_scan_kernel<T, ALIGNED, BWD, R, true>, a, slices);
+    auto go = [&](auto kernel) {
+        cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Sm::bytes(size));
+        if (err != cudaSuccess) return err;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(rows * size));
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = Sm::bytes(size);
+        cfg.stream = stream;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = size;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = size > 1 ? 1 : 0;
+        return cudaLaunchKernelEx(&cfg, kernel, a, slices);
+    };
+    return size > 1 ? go(recurrence_scan_kernel<T, ALIGN, BWD, R, true>) : go(recurrence_scan_kernel<T, ALIGN, BWD, R, false>);
 }
 
 template <bool BWD> cudaError_t launch_scan_any(const RecurrenceArgs& a, cudaStream_t stream) {
-    const bool aligned = a.D % (a.bf16 ? 8 : 4) == 0;  // then every row begins on 16 bytes
-    if (a.bf16)
-        return aligned ? launch_scan<__nv_bfloat16, true, BWD>(a, stream) : launch_scan<__nv_bfloat16, false, BWD>(a, stream);
-    return aligned ? launch_scan<float, true, BWD>(a, stream) : launch_scan<float, false, BWD>(a, stream);
+    const long long row = (long long)a.D * (a.bf16 ? 2 : 4);  // bytes of a row: the first begins on 16
+    if (a.bf16) {
+        if (row % 16 == 0) return launch_scan<__nv_bfloat16, 16, BWD>(a, stream);
+        return row % 4 == 0 ? launch_scan<__nv_bfloat16, 4, BWD>(a, stream) : launch_scan<__nv_bfloat16, 2, BWD>(a, stream);
+    }
+    return row % 16 == 0 ? launch_scan<float, 16, BWD>(a, stream) : launch_scan<float, 4, BWD>(a, stream);
 }
 
 }  // namespace
