@@ -90,28 +90,56 @@ __device__ __forceinline__ void cp_async4(void* dst, const void* src, bool on) {
                  : "memory");
 }
 
-// One row's channels of this thread into its 16 bytes at `to`; zeros where `on` is false or past the last channel.
+// One row's channels of this thread; zeros where `on` is false or past the last channel.
 template <typename T, int ALIGN>
-__device__ __forceinline__ void copy_row(uint4* to, const T* row, int c0, int col, int D, bool on) {
+__device__ __forceinline__ Pack<T> read_row(const T* row, int c0, int col, int D, bool on) {
     constexpr int P = 4 / sizeof(T);
+    Pack<T> r;
+    r.w[0] = r.w[1] = r.w[2] = r.w[3] = 0u;
     if constexpr (ALIGN == 16) {
         const int c = c0 + col * Pack<T>::V;
-        cp_async16(to, row + c, on && c < D);
+        if (on && c < D) r = Pack<T>::of(__ldcs(reinterpret_cast<const uint4*>(row + c)));
     } else if constexpr (ALIGN == 4) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int c = c0 + (col + 8 * j) * P;
-            cp_async4(reinterpret_cast<uint32_t*>(to) + j, row + c, on && c < D);
+            if (on && c < D) r.w[j] = __ldcs(reinterpret_cast<const unsigned*>(row + c));
         }
     } else {
-        uint32_t w[4] = {};
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const int c = c0 + col + 8 * e;
-            if (on && c < D) w[e >> 1] |= (uint32_t)reinterpret_cast<const unsigned short*>(row)[c] << (e & 1 ? 16 : 0);
+            if (on && c < D) r.w[e >> 1] |= (uint32_t)__ldcs(reinterpret_cast<const unsigned short*>(row) + c) << (e & 1 ? 16 : 0);
         }
-        *to = make_uint4(w[0], w[1], w[2], w[3]);
     }
+    return r;
+}
+
+// The same into this thread's 16 bytes of a slot of kThreads uint4, without waiting. Word by word the words of all
+// threads lie side by side, so that copying and reading back meet no bank twice.
+template <typename T, int ALIGN>
+__device__ __forceinline__ void copy_row(uint4* slot, const T* row, int c0, int col, int D, bool on) {
+    constexpr int P = 4 / sizeof(T);
+    if constexpr (ALIGN == 16) {
+        const int c = c0 + col * Pack<T>::V;
+        cp_async16(slot + threadIdx.x, row + c, on && c < D);
+    } else if constexpr (ALIGN == 4) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int c = c0 + (col + 8 * j) * P;
+            cp_async4(reinterpret_cast<uint32_t*>(slot) + j * kThreads + threadIdx.x, row + c, on && c < D);
+        }
+    } else {
+        const Pack<T> r = read_row<T, ALIGN>(row, c0, col, D, on);
+        slot[threadIdx.x] = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+    }
+}
+template <typename T, int ALIGN> __device__ __forceinline__ Pack<T> slot_of(const uint4* slot) {
+    if constexpr (ALIGN != 4) return Pack<T>::of(slot[threadIdx.x]);
+    Pack<T> r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r.w[j] = reinterpret_cast<const uint32_t*>(slot)[j * kThreads + threadIdx.x];
+    return r;
 }
 
 template <typename T, int ALIGN>
@@ -148,11 +176,10 @@ __device__ __forceinline__ void store_row(T* row, int c0, int col, int D, const 
 
 // Shared memory: the ring of stages, the spans of the token groups, the states that enter them, and the spans of the
 // parts of all CTAs of the cluster, by parity of the tile.
-template <typename T, bool BWD, int R> struct ScanSmem {
+template <typename T, int R> struct ScanSmem {
     static constexpr int CT = 8 * Pack<T>::V;              // channels of a slice
     static constexpr int kParts = kThreads / CT, kPer = kGroups / kParts;
-    static constexpr int kStreams = BWD ? 3 : 2;
-    static constexpr int kStage = kStreams * R * kThreads * 16, kStages = 2;
+    static constexpr int kStage = 2 * R * kThreads * 16, kStages = 2;
     static constexpr int kSpans = kGroups * CT * (int)sizeof(float2), kStates = kGroups * CT * (int)sizeof(float);
     static constexpr int kRank = kParts * CT * (int)sizeof(float2);
     static constexpr int bytes(int size) { return kStages * kStage + kSpans + kStates + 2 * size * kRank; }
@@ -161,7 +188,7 @@ template <typename T, bool BWD, int R> struct ScanSmem {
 // R: tokens of a thread. CLUSTER: the cluster has more than one CTA.
 template <typename T, int ALIGN, bool BWD, int R, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads, 2) recurrence_scan_kernel(RecurrenceArgs a, int slices) {
-    using Sm = ScanSmem<T, BWD, R>;
+    using Sm = ScanSmem<T, R>;
     constexpr int V = Pack<T>::V, CT = Sm::CT, TILE = kGroups * R, PARTS = Sm::kParts, PER = Sm::kPer, S = Sm::kStages;
     extern __shared__ __align__(16) unsigned char smem[];
     uint4* ring = reinterpret_cast<uint4*>(smem);
@@ -199,15 +226,13 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_scan_kernel(Recurrence
         return at < (unsigned)len ? (BWD ? len - 1 - (int)at : (int)at) : -1;
     };
     auto fetch = [&](int tile) {
-        uint4* to = ring + (size_t)(tile & 1) * (Sm::kStage / 16) + tid;
+        uint4* to = ring + (tile & 1) * (Sm::kStage / 16);
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             const int t = token(tile, i);
             const long long row = (long long)max(t, 0) * D;
-            copy_row<T, ALIGN>(to + (i * Sm::kStreams) * kThreads, la + row, c0, col, D, t >= 0);
-            copy_row<T, ALIGN>(to + (i * Sm::kStreams + 1) * kThreads, x + row, c0, col, D, t >= 0);
-            if constexpr (BWD)  // h_{t-1}
-                copy_row<T, ALIGN>(to + (i * Sm::kStreams + 2) * kThreads, hf + row - (t > 0 ? D : 0), c0, col, D, t > 0);
+            copy_row<T, ALIGN>(to + (2 * i) * kThreads, la + row, c0, col, D, t >= 0);
+            copy_row<T, ALIGN>(to + (2 * i + 1) * kThreads, x + row, c0, col, D, t >= 0);
         }
     };
     const long long step = (long long)size * TILE;
@@ -221,13 +246,19 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_scan_kernel(Recurrence
         cp_async_wait<S - 1>();
         F2 d[R][V / 2], A[V / 2], H[V / 2];
         Pack<T> px[R], ph[BWD ? R : 1];
-        {
-            const uint4* from = ring + (size_t)(tile & 1) * (Sm::kStage / 16) + tid;
+        if constexpr (BWD) {  // h_{t-1}: read now, used at the tile's end
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-                const Pack<T> pl = Pack<T>::of(from[(i * Sm::kStreams) * kThreads]);
-                px[i] = Pack<T>::of(from[(i * Sm::kStreams + 1) * kThreads]);
-                if constexpr (BWD) ph[i] = Pack<T>::of(from[(i * Sm::kStreams + 2) * kThreads]);
+                const int t = token(tile, i);
+                ph[i] = read_row<T, ALIGN>(hf + (long long)max(t - 1, 0) * D, c0, col, D, t > 0);
+            }
+        }
+        {
+            const uint4* from = ring + (tile & 1) * (Sm::kStage / 16);
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const Pack<T> pl = slot_of<T, ALIGN>(from + (2 * i) * kThreads);
+                px[i] = slot_of<T, ALIGN>(from + (2 * i + 1) * kThreads);
 #pragma unroll
                 for (int e = 0; e < V / 2; ++e) {
                     d[i][e] = f2(decay<T>(pl.get(2 * e)), decay<T>(pl.get(2 * e + 1)));
@@ -340,8 +371,8 @@ __global__ void recurrence_step_kernel(const T* log_alpha, const T* x, const flo
 
 template <typename T, int ALIGN, bool BWD>
 cudaError_t launch_scan(const RecurrenceArgs& a, cudaStream_t stream) {
-    constexpr int R = BWD ? 2 : 4;
-    using Sm = ScanSmem<T, BWD, R>;
+    constexpr int R = 4;
+    using Sm = ScanSmem<T, R>;
     const int slices = (a.D + Sm::CT - 1) / Sm::CT;
     const long long rows = (long long)a.N * slices;
     // CTAs of a cluster: as many as fill two CTAs on each SM, no more than the tokens give tiles to
