@@ -115,30 +115,46 @@ __device__ __forceinline__ Pack<T> read_row(const T* row, int c0, int col, int D
     return r;
 }
 
-// The same into this thread's 16 bytes of a slot of kThreads uint4, without waiting. Word by word the words of all
-// threads lie side by side, so that copying and reading back meet no bank twice.
-template <typename T, int ALIGN>
-__device__ __forceinline__ void copy_row(uint4* slot, const T* row, int c0, int col, int D, bool on) {
+// Stage `slot` ([token of the tile][32 words]) gets this warp's 4 R tokens of one tensor, without waiting; `row_of`
+// gives a token's row, or null. With 16-byte rows every thread copies what it will read; with 4-byte rows a warp
+// copies one token's 32 words at a time, because copies that touch four rows at once are bound by the load unit (the
+// readers then need __syncwarp). Words are swizzled by token group, so that the four groups of a warp read different
+// banks.
+template <typename T, int ALIGN, int R, typename F>
+__device__ __forceinline__ void copy_tile(uint32_t* slot, F row_of, int c0, int D) {
     constexpr int P = 4 / sizeof(T);
-    if constexpr (ALIGN == 16) {
-        const int c = c0 + col * Pack<T>::V;
-        cp_async16(slot + threadIdx.x, row + c, on && c < D);
-    } else if constexpr (ALIGN == 4) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = lane & 7;
+    if constexpr (ALIGN == 4) {
+        const int c = c0 + lane * P;
+        uint32_t* to = slot + warp * 4 * R * 32;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int c = c0 + (col + 8 * j) * P;
-            cp_async4(reinterpret_cast<uint32_t*>(slot) + j * kThreads + threadIdx.x, row + c, on && c < D);
+        for (int k = 0; k < 4 * R; ++k) {
+            const T* row = row_of(warp * 4 * R + k);
+            cp_async4(to + k * 32 + (lane ^ (8 * (k / R))), row + c, row && c < D);
         }
     } else {
-        const Pack<T> r = read_row<T, ALIGN>(row, c0, col, D, on);
-        slot[threadIdx.x] = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const T* row = row_of((threadIdx.x >> 3) * R + i);
+            uint4* to = reinterpret_cast<uint4*>(slot) + i * kThreads + threadIdx.x;
+            if constexpr (ALIGN == 16) {
+                const int c = c0 + col * Pack<T>::V;
+                cp_async16(to, row + c, row && c < D);
+            } else {
+                const Pack<T> r = read_row<T, ALIGN>(row, c0, col, D, row != nullptr);
+                *to = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+            }
+        }
     }
 }
-template <typename T, int ALIGN> __device__ __forceinline__ Pack<T> slot_of(const uint4* slot) {
-    if constexpr (ALIGN != 4) return Pack<T>::of(slot[threadIdx.x]);
+// This thread's channels of its token i.
+template <typename T, int ALIGN, int R> __device__ __forceinline__ Pack<T> slot_of(const uint32_t* slot, int i) {
+    if constexpr (ALIGN != 4) return Pack<T>::of(reinterpret_cast<const uint4*>(slot)[i * kThreads + threadIdx.x]);
+    const int col = threadIdx.x & 7, group = threadIdx.x >> 3;
+    const uint32_t* at = slot + (group * R + i) * 32;
     Pack<T> r;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) r.w[j] = reinterpret_cast<const uint32_t*>(slot)[j * kThreads + threadIdx.x];
+    for (int j = 0; j < 4; ++j) r.w[j] = at[(col + 8 * j) ^ (8 * (group & 3))];
     return r;
 }
 
@@ -191,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_scan_kernel(Recurrence
     using Sm = ScanSmem<T, R>;
     constexpr int V = Pack<T>::V, CT = Sm::CT, TILE = kGroups * R, PARTS = Sm::kParts, PER = Sm::kPer, S = Sm::kStages;
     extern __shared__ __align__(16) unsigned char smem[];
-    uint4* ring = reinterpret_cast<uint4*>(smem);
+    uint32_t* ring = reinterpret_cast<uint32_t*>(smem);
     float4* spans = reinterpret_cast<float4*>(smem + S * Sm::kStage);                  // [group][pair of V/2][col]: A, H, A, H
     float* states = reinterpret_cast<float*>(smem + S * Sm::kStage + Sm::kSpans);      // [group][quad of V/4][col][4]
     float2* ranks = reinterpret_cast<float2*>(smem + S * Sm::kStage + Sm::kSpans + Sm::kStates);  // [parity][rank][part][channel]
@@ -220,20 +236,22 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_scan_kernel(Recurrence
     float state = pc < D && a.state0 ? a.state0[(long long)n * D + pc] : 0.f;
     if constexpr (CLUSTER) cg::this_cluster().sync();  // every CTA has started, and has read its state
 
-    // token of this thread's step i in tile `tile`, in walking order; -1: past the end
-    auto token = [&](int tile, int i) {
-        const unsigned at = (unsigned)(tile * size + rank) * TILE + group * R + i;  // below len + 8 TILE: no wrap
+    // token k of this CTA's tile `tile`, in walking order; -1: past the end
+    auto token = [&](int tile, int k) {
+        const unsigned at = (unsigned)(tile * size + rank) * TILE + k;  // below len + 8 TILE: no wrap
         return at < (unsigned)len ? (BWD ? len - 1 - (int)at : (int)at) : -1;
     };
+    constexpr int kSlot = R * kThreads * 4;  // words of one tensor's tile
     auto fetch = [&](int tile) {
-        uint4* to = ring + (tile & 1) * (Sm::kStage / 16);
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const int t = token(tile, i);
-            const long long row = (long long)max(t, 0) * D;
-            copy_row<T, ALIGN>(to + (2 * i) * kThreads, la + row, c0, col, D, t >= 0);
-            copy_row<T, ALIGN>(to + (2 * i + 1) * kThreads, x + row, c0, col, D, t >= 0);
-        }
+        uint32_t* to = ring + (tile & 1) * 2 * kSlot;
+        auto from = [&](const T* base) {
+            return [=](int k) {
+                const int t = token(tile, k);
+                return t < 0 ? nullptr : base + (long long)t * D;
+            };
+        };
+        copy_tile<T, ALIGN, R>(to, from(la), c0, D);
+        copy_tile<T, ALIGN, R>(to + kSlot, from(x), c0, D);
     };
     const long long step = (long long)size * TILE;
     const int tiles = (int)((len + step - 1) / step);
@@ -244,21 +262,22 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_scan_kernel(Recurrence
     for (int tile = 0; tile < tiles; ++tile) {
         // 1. this thread's tokens as one span
         cp_async_wait<S - 1>();
+        if constexpr (ALIGN == 4) __syncwarp();
         F2 d[R][V / 2], A[V / 2], H[V / 2];
         Pack<T> px[R], ph[BWD ? R : 1];
         if constexpr (BWD) {  // h_{t-1}: read now, used at the tile's end
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-                const int t = token(tile, i);
+                const int t = token(tile, group * R + i);
                 ph[i] = read_row<T, ALIGN>(hf + (long long)max(t - 1, 0) * D, c0, col, D, t > 0);
             }
         }
         {
-            const uint4* from = ring + (tile & 1) * (Sm::kStage / 16);
+            const uint32_t* from = ring + (tile & 1) * 2 * kSlot;
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-                const Pack<T> pl = slot_of<T, ALIGN>(from + (2 * i) * kThreads);
-                px[i] = slot_of<T, ALIGN>(from + (2 * i + 1) * kThreads);
+                const Pack<T> pl = slot_of<T, ALIGN, R>(from, i);
+                px[i] = slot_of<T, ALIGN, R>(from + kSlot, i);
 #pragma unroll
                 for (int e = 0; e < V / 2; ++e) {
                     d[i][e] = f2(decay<T>(pl.get(2 * e)), decay<T>(pl.get(2 * e + 1)));
@@ -273,6 +292,7 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_scan_kernel(Recurrence
                 }
             }
         }
+        if constexpr (ALIGN == 4) __syncwarp();
         if (tile + S < tiles) fetch(tile + S);
         cp_async_commit();
 #pragma unroll
@@ -324,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_scan_kernel(Recurrence
         }
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            const int t = token(tile, i);
+            const int t = token(tile, group * R + i);
             float y[V], z[V];
 #pragma unroll
             for (int e = 0; e < V / 2; ++e) {
