@@ -16,9 +16,9 @@
 // barrier is due) and then
 //   1. composes its tokens into one span (A, H) and leaves it in shared memory;
 //   2. as (channel, part) composes the spans of one part of the CTA's token
-//      groups, and hands the part's span to every CTA of the cluster;
-//   3. walks the parts before its own, which gives the state that enters each of
-//      its groups, and leaves these in shared memory;
+//      groups, then the parts' spans, and leaves the CTA's to the cluster;
+//   3. walks the CTAs and parts before its own, which gives the state that enters
+//      each of its groups, and leaves these in shared memory;
 //   4. runs its tokens again from the state that enters them and writes them.
 // The sequential depth is T / (tokens of a cluster's tile). Nothing waits on a
 // flag, and the order of every product and sum is fixed by the sizes alone.
@@ -197,9 +197,17 @@ template <typename T, int R> struct ScanSmem {
     static constexpr int kParts = kThreads / CT, kPer = kGroups / kParts;
     static constexpr int kStage = 2 * R * kThreads * 16, kStages = 2;
     static constexpr int kSpans = kGroups * CT * (int)sizeof(float2), kStates = kGroups * CT * (int)sizeof(float);
-    static constexpr int kRank = kParts * CT * (int)sizeof(float2);
-    static constexpr int bytes(int size) { return kStages * kStage + kSpans + kStates + 2 * size * kRank; }
+    static constexpr int kBytes = kStages * kStage + kSpans + kStates + (kParts + 2) * CT * (int)sizeof(float2);
 };
+
+// A cluster barrier that publishes this thread's writes to its own CTA's shared memory, and them alone: the full
+// release would wait for the tile's stores to global memory, 1.5 us.
+__device__ __forceinline__ void cluster_exchange() {
+    asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
+}
 
 // R: tokens of a thread. CLUSTER: the cluster has more than one CTA.
 template <typename T, int ALIGN, bool BWD, int R, bool CLUSTER>
@@ -210,7 +218,8 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_scan_kernel(Recurrence
     uint32_t* ring = reinterpret_cast<uint32_t*>(smem);
     float4* spans = reinterpret_cast<float4*>(smem + S * Sm::kStage);                  // [group][pair of V/2][col]: A, H, A, H
     float* states = reinterpret_cast<float*>(smem + S * Sm::kStage + Sm::kSpans);      // [group][quad of V/4][col][4]
-    float2* ranks = reinterpret_cast<float2*>(smem + S * Sm::kStage + Sm::kSpans + Sm::kStates);  // [parity][rank][part][channel]
+    float2* parts = reinterpret_cast<float2*>(smem + S * Sm::kStage + Sm::kSpans + Sm::kStates);  // [part][channel]
+    float2* whole_of = parts + PARTS * CT;  // [parity][channel]: the CTA's span, read by the cluster
     const int tid = threadIdx.x, col = tid & 7, group = tid >> 3;
     int rank = 0, size = 1;
     long long id = blockIdx.x;
@@ -301,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_scan_kernel(Recurrence
             spans[(group * (V / 2) + e) * 8 + col] = make_float4(A_.x, H_.x, A_.y, H_.y);
         }
         __syncthreads();
-        // 2. as (channel, part): the part's span, to every CTA of the cluster
+        // 2. as (channel, part): the part's span, the CTA's
         float2 w[PER];
 #pragma unroll
         for (int k = 0; k < PER; ++k)
@@ -309,25 +318,35 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_scan_kernel(Recurrence
         float2 all = w[0];
 #pragma unroll
         for (int k = 1; k < PER; ++k) all = make_float2(all.x * w[k].x, fmaf(w[k].x, all.y, w[k].y));
-        float2* mine = ranks + ((size_t)(tile & 1) * size + rank) * PARTS * CT + part * CT + p;
-        if constexpr (CLUSTER) {
-            const cg::cluster_group cl = cg::this_cluster();
-            for (int r = 0; r < size; ++r) *cl.map_shared_rank(mine, r) = all;
-            cl.sync();
-        } else {
-            *mine = all;
-            __syncthreads();
+        parts[part * CT + p] = all;
+        __syncthreads();
+        float2 before = make_float2(1.f, 0.f), whole = before;  // of the CTA's parts: those before this one, all
+#pragma unroll
+        for (int k = 0; k < PARTS; ++k) {
+            const float2 u = parts[k * CT + p];
+            if (k == part) before = whole;
+            whole = make_float2(whole.x * u.x, fmaf(u.x, whole.y, u.y));
         }
         // 3. the state that enters this part's groups; the state after the cluster's tile
-        const float2* theirs = ranks + (size_t)(tile & 1) * size * PARTS * CT + p;
-        float s = 0.f;
-        for (int r = 0; r < size; ++r)
+        float s = state;
+        if constexpr (CLUSTER) {
+            float2* mine = whole_of + (tile & 1) * CT + p;
+            if (part == 0) *mine = whole;
+            cluster_exchange();
+            float2 u[kMaxCluster];
 #pragma unroll
-            for (int k = 0; k < PARTS; ++k) {
-                if (r == rank && k == part) s = state;
-                const float2 u = theirs[(r * PARTS + k) * CT];
-                state = fmaf(u.x, state, u.y);
-            }
+            for (int r = 0; r < kMaxCluster; ++r)
+                if (r < size) u[r] = *cg::this_cluster().map_shared_rank(mine, r);
+#pragma unroll
+            for (int r = 0; r < kMaxCluster; ++r)
+                if (r < size) {
+                    if (r == rank) s = state;
+                    state = fmaf(u[r].x, state, u[r].y);
+                }
+        } else {
+            state = fmaf(whole.x, state, whole.y);
+        }
+        s = fmaf(before.x, s, before.y);
 #pragma unroll
         for (int k = 0; k < PER; ++k) {
             states[(((part * PER + k) * (V / 4) + pair / 2) * 8 + pcol) * 4 + (pair & 1) * 2 + half] = s;
@@ -376,6 +395,7 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_scan_kernel(Recurrence
         }
     }
     cp_async_wait<0>();
+    if constexpr (CLUSTER) cg::this_cluster().sync();  // no CTA ends while another reads its shared memory
     if (part == 0 && rank == 0 && pc < D && a.state_end) a.state_end[(long long)n * D + pc] = state;
 }
 
@@ -400,12 +420,12 @@ cudaError_t launch_scan(const RecurrenceArgs& a, cudaStream_t stream) {
     int size = 1;
     while (size < kMaxCluster && rows * size * 2 <= 2 * 148 && (long long)size * kGroups * R < tokens) size *= 2;
     auto go = [&](auto kernel) {
-        cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Sm::bytes(size));
+        cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Sm::kBytes);
         if (err != cudaSuccess) return err;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(rows * size));
         cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = Sm::bytes(size);
+        cfg.dynamicSmemBytes = Sm::kBytes;
         cfg.stream = stream;
         cudaLaunchAttribute attr;
         attr.id = cudaLaunchAttributeClusterDimension;
