@@ -76,12 +76,10 @@ template <> __device__ __forceinline__ float decay<__nv_bfloat16>(float x) {
 
 // ALIGN: what every row's first byte is a multiple of, 16, 4 or (bf16 alone) 2. It sets a thread's channels within the
 // slice: 16 bytes at once; else 4-byte words eight apart, so that the eight threads of a token group touch neighbouring
-// words; else single elements eight apart.
+// words.
 template <typename T, int ALIGN> __device__ __forceinline__ int channel_of(int col, int e) {
     constexpr int V = Pack<T>::V, P = 4 / sizeof(T);  // elements of a word
-    if (ALIGN == 16) return col * V + e;
-    if (ALIGN == 4) return (col + 8 * (e / P)) * P + e % P;
-    return col + 8 * e;
+    return ALIGN == 16 ? col * V + e : (col + 8 * (e / P)) * P + e % P;
 }
 
 __device__ __forceinline__ void cp_async4(void* dst, const void* src, bool on) {
@@ -108,53 +106,92 @@ __device__ __forceinline__ Pack<T> read_row(const T* row, int c0, int col, int D
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const int c = c0 + col + 8 * e;
+            const int c = c0 + channel_of<T, ALIGN>(col, e);
             if (on && c < D) r.w[e >> 1] |= (uint32_t)__ldcs(reinterpret_cast<const unsigned short*>(row) + c) << (e & 1 ? 16 : 0);
         }
     }
     return r;
 }
 
-// Stage `slot` ([token of the tile][32 words]) gets this warp's 4 R tokens of one tensor, without waiting; `row_of`
-// gives a token's row, or null. With 16-byte rows every thread copies what it will read; with 4-byte rows a warp
-// copies one token's 32 words at a time, because copies that touch four rows at once are bound by the load unit (the
-// readers then need __syncwarp). Words are swizzled by token group, so that the four groups of a warp read different
-// banks.
-template <typename T, int ALIGN, int R, typename F>
-__device__ __forceinline__ void copy_tile(uint32_t* slot, F row_of, int c0, int D) {
+// Stage `slot` ([token of the tile][32 words], then one more word a token) gets this warp's 4 R tokens of one tensor,
+// without waiting. `first`: the row of the CTA's first token; `step`: from a token to the next (D or -D); `left`: the
+// number of tokens there are. With 16-byte rows every thread copies what it will read; else a warp copies one token's 32
+// words at a time, because copies that touch four rows at once are bound by the load unit (the readers then need
+// __syncwarp). Words are swizzled by token group, so that the four groups of a warp read different banks. Rows that
+// begin in the middle of a word (ALIGN 2, every other row) are copied from that word on, 33 words, and shifted by the
+// reader; a word that reaches past the tensor's end `stop` is read by halves.
+template <typename T, int ALIGN, int R>
+__device__ __forceinline__ void copy_tile(uint32_t* slot, const T* first, int step, int left, int c0, int D, const T* stop) {
     constexpr int P = 4 / sizeof(T);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = lane & 7;
+    if constexpr (ALIGN == 16) {
+        const int k0 = (threadIdx.x >> 3) * R, c = c0 + col * Pack<T>::V;
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            cp_async16(reinterpret_cast<uint4*>(slot) + i * kThreads + threadIdx.x, first + (long long)(k0 + i) * step + c,
+                       k0 + i < left && c < D);
+        return;
+    }
+    const int k0 = warp * 4 * R;
+    uint32_t* to = slot + k0 * 32;
+    left -= k0;
     if constexpr (ALIGN == 4) {
         const int c = c0 + lane * P;
-        uint32_t* to = slot + warp * 4 * R * 32;
+        if (c >= D) left = 0;
+        const T* row = first + (long long)k0 * step + c;
 #pragma unroll
-        for (int k = 0; k < 4 * R; ++k) {
-            const T* row = row_of(warp * 4 * R + k);
-            cp_async4(to + k * 32 + (lane ^ (8 * (k / R))), row + c, row && c < D);
-        }
+        for (int k = 0; k < 4 * R; ++k, row += step) cp_async4(to + k * 32 + (lane ^ (8 * (k / R))), row, k < left);
     } else {
+        const int n = min(D - c0, 64);
+        const char* at = reinterpret_cast<const char*>(first + (long long)k0 * step + c0);
+        // the word that holds the tensor's last element may lie in this warp's rows
+        const char* last = step > 0 ? at + 2ll * step * (min(left, 4 * R) - 1) : at;
+        const bool ends = left > 0 && last + 4 * 33 > reinterpret_cast<const char*>(stop);
+        const int left0 = 2 * lane < n ? left : 0, left1 = 2 * lane - 1 < n ? left : 0;  // rows that need this lane's word
+        {
+            const char* mine = at + 2ll * step * lane;  // lane k: the 33rd word of row k
+            if (lane < 4 * R && (reinterpret_cast<uintptr_t>(mine) & 2)) {
+                const char* w = mine - 2 + 128;
+                const bool on = lane < left && n == 64;
+                uint32_t* dst = slot + kGroups * R * 32 + k0 + lane;
+                if (on && w + 4 > reinterpret_cast<const char*>(stop)) *dst = *reinterpret_cast<const unsigned short*>(w);
+                else cp_async4(dst, w, on);
+            }
+        }
+        if (!ends) {
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const T* row = row_of((threadIdx.x >> 3) * R + i);
-            uint4* to = reinterpret_cast<uint4*>(slot) + i * kThreads + threadIdx.x;
-            if constexpr (ALIGN == 16) {
-                const int c = c0 + col * Pack<T>::V;
-                cp_async16(to, row + c, row && c < D);
-            } else {
-                const Pack<T> r = read_row<T, ALIGN>(row, c0, col, D, row != nullptr);
-                *to = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+            for (int k = 0; k < 4 * R; ++k, at += 2ll * step) {
+                const uintptr_t w = reinterpret_cast<uintptr_t>(at);
+                cp_async4(to + k * 32 + (lane ^ (8 * (k / R))), reinterpret_cast<const char*>(w & ~(uintptr_t)2) + 4 * lane,
+                          k < (w & 2 ? left1 : left0));
+            }
+        } else {
+#pragma unroll 1
+            for (int k = 0; k < 4 * R; ++k, at += 2ll * step) {
+                const uintptr_t w = reinterpret_cast<uintptr_t>(at);
+                const char* from = reinterpret_cast<const char*>(w & ~(uintptr_t)2) + 4 * lane;
+                const bool on = k < (w & 2 ? left1 : left0);
+                uint32_t* dst = to + k * 32 + (lane ^ (8 * (k / R)));
+                if (on && from + 4 > reinterpret_cast<const char*>(stop)) *dst = *reinterpret_cast<const unsigned short*>(from);
+                else cp_async4(dst, from, on);
             }
         }
     }
 }
-// This thread's channels of its token i.
-template <typename T, int ALIGN, int R> __device__ __forceinline__ Pack<T> slot_of(const uint32_t* slot, int i) {
-    if constexpr (ALIGN != 4) return Pack<T>::of(reinterpret_cast<const uint4*>(slot)[i * kThreads + threadIdx.x]);
-    const int col = threadIdx.x & 7, group = threadIdx.x >> 3;
+// This thread's channels of its token i; `odd`: the row begins in the middle of a word.
+template <typename T, int ALIGN, int R> __device__ __forceinline__ Pack<T> slot_of(const uint32_t* slot, int i, bool odd) {
+    if constexpr (ALIGN == 16) return Pack<T>::of(reinterpret_cast<const uint4*>(slot)[i * kThreads + threadIdx.x]);
+    const int col = threadIdx.x & 7, group = threadIdx.x >> 3, turn = 8 * (group & 3);
     const uint32_t* at = slot + (group * R + i) * 32;
     Pack<T> r;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) r.w[j] = at[(col + 8 * j) ^ (8 * (group & 3))];
+    for (int j = 0; j < 4; ++j) {
+        const int k = col + 8 * j;
+        r.w[j] = at[k ^ turn];
+        if constexpr (ALIGN == 2) {
+            if (odd) r.w[j] = __funnelshift_r(r.w[j], k == 31 ? slot[kGroups * R * 32 + group * R + i] : at[(k + 1) ^ turn], 16);
+        }
+    }
     return r;
 }
 
@@ -195,7 +232,8 @@ __device__ __forceinline__ void store_row(T* row, int c0, int col, int D, const 
 template <typename T, int R> struct ScanSmem {
     static constexpr int CT = 8 * Pack<T>::V;              // channels of a slice
     static constexpr int kParts = kThreads / CT, kPer = kGroups / kParts;
-    static constexpr int kStage = 2 * R * kThreads * 16, kStages = 2;
+    static constexpr int kSlot = R * kThreads * 16 + kGroups * R * 4;  // one tensor's tile, and a word more a token
+    static constexpr int kStage = 2 * kSlot, kStages = 2;
     static constexpr int kSpans = kGroups * CT * (int)sizeof(float2), kStates = kGroups * CT * (int)sizeof(float);
     static constexpr int kBytes = kStages * kStage + kSpans + kStates + (kParts + 2) * CT * (int)sizeof(float2);
 };
@@ -250,17 +288,17 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_scan_kernel(Recurrence
         const unsigned at = (unsigned)(tile * size + rank) * TILE + k;  // below len + 8 TILE: no wrap
         return at < (unsigned)len ? (BWD ? len - 1 - (int)at : (int)at) : -1;
     };
-    constexpr int kSlot = R * kThreads * 4;  // words of one tensor's tile
+    constexpr int kSlot = Sm::kSlot / 4;
+    // the end of the tensors, for ALIGN 2
+    const long long cells = (a.cu_seqlens ? 1ll : (long long)a.N) * a.T * D;
+    const T *la_stop = (const T*)a.log_alpha + cells, *x_stop = (const T*)a.x + cells;
     auto fetch = [&](int tile) {
         uint32_t* to = ring + (tile & 1) * 2 * kSlot;
-        auto from = [&](const T* base) {
-            return [=](int k) {
-                const int t = token(tile, k);
-                return t < 0 ? nullptr : base + (long long)t * D;
-            };
-        };
-        copy_tile<T, ALIGN, R>(to, from(la), c0, D);
-        copy_tile<T, ALIGN, R>(to + kSlot, from(x), c0, D);
+        const long long at = (long long)(tile * size + rank) * TILE;
+        const int left = (int)min(max(len - at, 0ll), (long long)TILE);
+        const long long row = (BWD ? len - 1 - at : at) * D;
+        copy_tile<T, ALIGN, R>(to, la + row, BWD ? -D : D, left, c0, D, la_stop);
+        copy_tile<T, ALIGN, R>(to + kSlot, x + row, BWD ? -D : D, left, c0, D, x_stop);
     };
     const long long step = (long long)size * TILE;
     const int tiles = (int)((len + step - 1) / step);
@@ -271,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_scan_kernel(Recurrence
     for (int tile = 0; tile < tiles; ++tile) {
         // 1. this thread's tokens as one span
         cp_async_wait<S - 1>();
-        if constexpr (ALIGN == 4) __syncwarp();
+        if constexpr (ALIGN != 16) __syncwarp();
         F2 d[R][V / 2], A[V / 2], H[V / 2];
         Pack<T> px[R], ph[BWD ? R : 1];
         if constexpr (BWD) {  // h_{t-1}: read now, used at the tile's end
@@ -285,8 +323,12 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_scan_kernel(Recurrence
             const uint32_t* from = ring + (tile & 1) * 2 * kSlot;
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-                const Pack<T> pl = slot_of<T, ALIGN, R>(from, i);
-                px[i] = slot_of<T, ALIGN, R>(from + kSlot, i);
+                // D is odd and the tensors begin on 16 bytes: every other row begins in the middle of a word
+                // (those past the end, which hold zeros, counted on: the copy goes by the same rows)
+                const int at = (tile * size + rank) * TILE + group * R + i;
+                const bool odd = ALIGN == 2 && (((int)begin + (BWD ? len - 1 - at : at)) & 1);
+                const Pack<T> pl = slot_of<T, ALIGN, R>(from, i, odd);
+                px[i] = slot_of<T, ALIGN, R>(from + kSlot, i, odd);
 #pragma unroll
                 for (int e = 0; e < V / 2; ++e) {
                     d[i][e] = f2(decay<T>(pl.get(2 * e)), decay<T>(pl.get(2 * e + 1)));
@@ -301,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_scan_kernel(Recurrence
                 }
             }
         }
-        if constexpr (ALIGN == 4) __syncwarp();
+        if constexpr (ALIGN != 16) __syncwarp();
         if (tile + S < tiles) fetch(tile + S);
         cp_async_commit();
 #pragma unroll
@@ -415,10 +457,12 @@ cudaError_t launch_scan(const RecurrenceArgs& a, cudaStream_t stream) {
     using Sm = ScanSmem<T, R>;
     const int slices = (a.D + Sm::CT - 1) / Sm::CT;
     const long long rows = (long long)a.N * slices;
-    // CTAs of a cluster: as many as fill two CTAs on each SM, no more than the tokens give tiles to
+    // CTAs of a cluster: one where that nearly fills the SMs (128 rows, T 8192, D 4096 backward: 127 us, with two 131);
+    // else as many as fill two CTAs on each SM (64 rows, T 4096: 24 us with four, 31 with two, 40 with one), no more than
+    // the tokens give tiles to.
     const long long tokens = a.cu_seqlens ? (a.T + a.N - 1) / a.N : a.T;
     int size = 1;
-    while (size < kMaxCluster && rows * size * 2 <= 2 * 148 && (long long)size * kGroups * R < tokens) size *= 2;
+    while (rows < 128 && size < kMaxCluster && rows * size * 2 <= 2 * 148 && (long long)size * kGroups * R < tokens) size *= 2;
     auto go = [&](auto kernel) {
         cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Sm::kBytes);
         if (err != cudaSuccess) return err;
