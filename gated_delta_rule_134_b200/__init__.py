@@ -11,6 +11,7 @@ cannot be loaded, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 __all__ = ["load", "chunk_fwd", "chunk_fwd_varlen", "chunk_bwd", "chunk_fwd_noalloc", "noalloc_status", "decode_step",
@@ -122,10 +123,11 @@ def _ptr(t):
 
 def _dtype_of(t) -> str:
     import torch
-    if t.dtype == torch.float32:
-        return "f32"
-    if t.dtype == torch.bfloat16:
+    dt = t.dtype
+    if dt == torch.bfloat16:
         return "bf16"
+    if dt == torch.float32:
+        return "f32"
     raise TypeError(f"unsupported dtype {t.dtype}; use float32 or bfloat16")
 
 
@@ -570,34 +572,45 @@ def _heads_view(t, name, lead, d, dt, dev):
 
 
 def _qk_args(q, k, q_weight, k_weight, cos, sin, positions, norm):
-    """Checks what the two directions share; (q view, k view, n, Hq, Hk, d, rot, max_pos, pos_bytes)."""
+    """Checks what the two directions share. Returns the pointers of q, k, weights, tables and positions, pos_bytes, and
+    the sizes and strides that follow the outputs in the C calls."""
     import torch
     if norm not in NORMS:
         raise ValueError(f"norm must be one of {sorted(NORMS)}")
-    if q.dim() < 3 or k.dim() != q.dim():
-        raise ValueError(f"q, k: expected [..., tokens, heads, d], got {tuple(q.shape)} and {tuple(k.shape)}")
-    dt, dev, lead, d = q.dtype, q.device, q.shape[:-2], q.shape[-1]
-    qv, kv = _heads_view(q, "q", lead, d, dt, dev), _heads_view(k, "k", lead, d, dt, dev)
-    n = qv.shape[0]
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _need(w, name, (d,), dt, dev)
+    qs, ks = q.shape, k.shape
+    if len(qs) < 3 or len(ks) != len(qs):
+        raise ValueError(f"q, k: expected [..., tokens, heads, d], got {tuple(qs)} and {tuple(ks)}")
+    dt, dev, d = q.dtype, q.device, qs[-1]
+    sq, sk = q.stride(), k.stride()
+    if not (len(qs) == 3 and q.is_cuda and sq[2] == sk[2] == 1 and ks[0] == qs[0] and ks[2] == d and k.dtype == dt
+            and k.device == dev):
+        q, k = _heads_view(q, "q", qs[:-2], d, dt, dev), _heads_view(k, "k", qs[:-2], d, dt, dev)
+        sq, sk = q.stride(), k.stride()
+    n = q.shape[0]
+    if q_weight is not None:
+        _need(q_weight, "q_weight", (d,), dt, dev)
+    if k_weight is not None:
+        _need(k_weight, "k_weight", (d,), dt, dev)
     rot = max_pos = pos_bytes = 0
     if positions is not None:
         if cos is None or sin is None:
             raise ValueError("positions need the cos and sin tables")
         if cos.dim() != 2:
             raise ValueError(f"cos: expected [max_pos, rot/2], got {tuple(cos.shape)}")
-        max_pos, rot = cos.shape[0], 2 * cos.shape[1]
-        _need(cos, "cos", (max_pos, rot // 2), torch.float32, dev)
-        _need(sin, "sin", (max_pos, rot // 2), torch.float32, dev)
-        if positions.dtype not in (torch.int32, torch.int64):
-            raise TypeError(f"positions: expected int32 or int64, got {positions.dtype}")
-        pos_bytes = positions.element_size()
+        table = cos.shape
+        max_pos, rot = table[0], 2 * table[1]
+        _need(cos, "cos", table, torch.float32, dev)
+        _need(sin, "sin", table, torch.float32, dev)
+        pos_dt = positions.dtype
+        if pos_dt != torch.int64 and pos_dt != torch.int32:
+            raise TypeError(f"positions: expected int32 or int64, got {pos_dt}")
+        pos_bytes = 8 if pos_dt == torch.int64 else 4
         if positions.numel() != n:
             raise ValueError(f"positions: expected one per token ({n}), got {tuple(positions.shape)}")
-        _need(positions, "positions", positions.shape, positions.dtype, dev)
-    return qv, kv, n, qv.shape[1], kv.shape[1], d, rot, max_pos, pos_bytes
+        _need(positions, "positions", positions.shape, pos_dt, dev)
+    return ((q.data_ptr(), k.data_ptr(), _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin), _ptr(positions),
+             pos_bytes),
+            (n, q.shape[1], k.shape[1], d, rot, max_pos, sq[0], sq[1], sk[0], sk[1], NORMS[norm]))
 
 
 def qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positions=None, *, norm: str = "rms",
@@ -615,7 +628,7 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positio
     import torch
     lib = load()
     dts = _dtype_of(q)
-    qv, kv, n, Hq, Hk, d, rot, max_pos, pos_bytes = _qk_args(q, k, q_weight, k_weight, cos, sin, positions, norm)
+    inputs, sizes = _qk_args(q, k, q_weight, k_weight, cos, sin, positions, norm)
     dt, dev = q.dtype, q.device
     if q_out is None:
         q_out = torch.empty(q.shape, dtype=dt, device=dev)
@@ -626,12 +639,15 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positio
     else:
         _need(k_out, "k_out", k.shape, dt, dev)
     with _on(dev):
-        code = lib.kda_qk_norm_rope(_ptr(qv), _ptr(kv), _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin),
-                                    _ptr(positions), pos_bytes, _ptr(q_out), _ptr(k_out), n, Hq, Hk, d, rot, max_pos,
-                                    qv.stride(0), qv.stride(1), kv.stride(0), kv.stride(1), NORMS[norm], eps, q_scale,
-                                    int(bool(interleaved)), _DTYPE[dts], _stream(stream, dev))
+        code = lib.kda_qk_norm_rope(*inputs, q_out.data_ptr(), k_out.data_ptr(), *sizes, eps, q_scale,
+                                    1 if interleaved else 0, _DTYPE[dts], _stream(stream, dev))
     _check("kda_qk_norm_rope", code)
     return q_out, k_out
+
+
+@functools.lru_cache(maxsize=256)
+def _qk_workspace_size(n, Hq, Hk, d) -> int:
+    return int(load().kda_qk_norm_rope_bwd_workspace_size(n, Hq, Hk, d))
 
 
 def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, cos=None, sin=None, positions=None, *,
@@ -644,31 +660,28 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, cos=Non
     import torch
     lib = load()
     dts = _dtype_of(q)
-    qv, kv, n, Hq, Hk, d, rot, max_pos, pos_bytes = _qk_args(q, k, q_weight, k_weight, cos, sin, positions, norm)
-    dt, dev = q.dtype, q.device
+    inputs, sizes = _qk_args(q, k, q_weight, k_weight, cos, sin, positions, norm)
+    dt, dev, d = q.dtype, q.device, q.shape[-1]
     _need(dq_out, "dq_out", q.shape, dt, dev)
     _need(dk_out, "dk_out", k.shape, dt, dev)
-    g = {"dq": torch.empty(q.shape, dtype=dt, device=dev), "dk": torch.empty(k.shape, dtype=dt, device=dev),
-         "dq_weight": None if q_weight is None else torch.empty(d, dtype=torch.float32, device=dev),
-         "dk_weight": None if k_weight is None else torch.empty(d, dtype=torch.float32, device=dev)}
-    if workspace is None and (q_weight is not None or k_weight is not None):
-        workspace = torch.empty(int(lib.kda_qk_norm_rope_bwd_workspace_size(n, Hq, Hk, d)), dtype=torch.uint8,
-                                device=dev)
+    dq, dk = torch.empty(q.shape, dtype=dt, device=dev), torch.empty(k.shape, dtype=dt, device=dev)
+    dqw = None if q_weight is None else torch.empty(d, dtype=torch.float32, device=dev)
+    dkw = None if k_weight is None else torch.empty(d, dtype=torch.float32, device=dev)
+    if workspace is None and (dqw is not None or dkw is not None):
+        workspace = torch.empty(_qk_workspace_size(*sizes[:4]), dtype=torch.uint8, device=dev)
     ws_len = 0 if workspace is None else workspace.numel() * workspace.element_size()
     with _on(dev):
-        code = lib.kda_qk_norm_rope_bwd(_ptr(dq_out), _ptr(dk_out), _ptr(qv), _ptr(kv), _ptr(q_weight),
-                                        _ptr(k_weight), _ptr(cos), _ptr(sin), _ptr(positions), pos_bytes,
-                                        _ptr(g["dq"]), _ptr(g["dk"]), _ptr(g["dq_weight"]), _ptr(g["dk_weight"]), n,
-                                        Hq, Hk, d, rot, max_pos, qv.stride(0), qv.stride(1), kv.stride(0),
-                                        kv.stride(1), NORMS[norm], eps, q_scale, int(bool(interleaved)), _DTYPE[dts],
-                                        _ptr(workspace), ws_len, _stream(stream, dev))
+        code = lib.kda_qk_norm_rope_bwd(dq_out.data_ptr(), dk_out.data_ptr(), *inputs, dq.data_ptr(), dk.data_ptr(),
+                                        _ptr(dqw), _ptr(dkw), *sizes, eps, q_scale, 1 if interleaved else 0,
+                                        _DTYPE[dts], _ptr(workspace), ws_len, _stream(stream, dev))
     _check("kda_qk_norm_rope_bwd", code)
-    return g
+    return {"dq": dq, "dk": dk, "dq_weight": dqw, "dk_weight": dkw}
 
 
 # ---------------------------------------------------------------- paged decode attention
 
 
+@functools.lru_cache(maxsize=256)
 def attn_decode_workspace_size(N, Hq, Hk, d) -> int:
     return int(load().kda_attn_decode_workspace_size(N, Hq, Hk, d))
 
@@ -713,7 +726,7 @@ def attn_decode(q, k_cache, v_cache, page_table, seq_lens, *, k=None, v=None, sc
         return_lse = True
     elif return_lse:
         lse = torch.empty(N, Hq, dtype=torch.float32, device=dev)
-    ws_bytes = int(lib.kda_attn_decode_workspace_size(N, Hq, Hk, d))
+    ws_bytes = attn_decode_workspace_size(N, Hq, Hk, d)
     if ws_bytes and workspace is None:
         workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
     ws_len = 0 if workspace is None else workspace.numel() * workspace.element_size()

@@ -22,8 +22,6 @@
 // pair and does not end it. attn_join_kernel joins the pieces in order. A warp
 // works for itself (no block barrier in the loop): it copies 16 rows of K and V
 // a stage with 16-byte cp.async, several stages ahead, across the ends of pairs.
-#include <atomic>
-
 #include "kda_common.cuh"
 #include "kda_internal.h"
 #include "kda_sm100.cuh"
@@ -732,17 +730,9 @@ static cudaError_t launch_attn(const AttnDecodeArgs& a, cudaStream_t stream) {
     using Geo = Geometry<T, D>;
     auto split = attn_split_kernel<T, D, NT>;
     const int G = a.Hq / a.Hk, pairs = a.N * a.Hk * ((G + kHeads - 1) / kHeads);
-    // The shared-memory limit is set once a device (a bit each; devices past 63 set it every time).
     static std::atomic<unsigned long long> raised{0};
-    int device = 0;
-    cudaError_t err = cudaGetDevice(&device);
+    cudaError_t err = allow_smem(split, Geo::kSmem, raised);
     if (err != cudaSuccess) return err;
-    const unsigned long long bit = device < 64 ? 1ull << device : 0;
-    if (!(raised.load(std::memory_order_relaxed) & bit)) {
-        err = cudaFuncSetAttribute(split, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo::kSmem);
-        if (err != cudaSuccess) return err;
-        raised.fetch_or(bit, std::memory_order_relaxed);
-    }
     split<<<Geo::kCtas, kWarps * 32, Geo::kSmem, stream>>>(a);
     if ((err = cudaGetLastError()) != cudaSuccess) return err;
     // The join is launched while the split kernel runs (programmatic dependent launch) and waits for its end.

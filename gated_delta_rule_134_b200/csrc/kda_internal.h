@@ -4,9 +4,25 @@
 #include <cuda_runtime.h>
 #include <stddef.h>
 
+#include <atomic>
+
 #include "kda.h"
 
 namespace kda {
+
+// Raises a kernel's limit of dynamic shared memory once a device (a bit each in
+// `raised`, a static of the caller for this kernel; devices past 63 every time).
+template <typename Kernel>
+inline cudaError_t allow_smem(Kernel kernel, int bytes, std::atomic<unsigned long long>& raised) {
+    int device = 0;
+    cudaError_t err = cudaGetDevice(&device);
+    if (err != cudaSuccess) return err;
+    const unsigned long long bit = device < 64 ? 1ull << device : 0;
+    if (raised.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (err == cudaSuccess) raised.fetch_or(bit, std::memory_order_relaxed);
+    return err;
+}
 
 struct ChunkArgs {
     const void *q, *k, *v, *log_alpha, *beta;

@@ -508,8 +508,9 @@ cudaError_t launch_qk_norm_rope_bwd(const QkArgs& a, cudaStream_t stream) {
             q_ctas = (int)std::min(q, useful(a.Hq));
             const int k_ctas = (int)std::min(kBwdCtas - q_ctas, useful(a.Hk));
             ctas = q_ctas + k_ctas;
+            static std::atomic<unsigned long long> raised[2];  // of this size and mode: float, bf16
             auto go = [&](auto kernel, int smem) {
-                const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+                const cudaError_t e = allow_smem(kernel, smem, raised[a.bf16]);
                 if (e != cudaSuccess) return e;
                 kernel<<<ctas, kThreads, smem, stream>>>(a, chunk_of(a.Hq), chunk_of(a.Hk), q_ctas, part);
                 return cudaGetLastError();

@@ -463,8 +463,9 @@ cudaError_t launch_scan(const RecurrenceArgs& a, cudaStream_t stream) {
     const long long tokens = a.cu_seqlens ? (a.T + a.N - 1) / a.N : a.T;
     int size = 1;
     while (rows < 128 && size < kMaxCluster && rows * size * 2 <= 2 * 148 && (long long)size * kGroups * R < tokens) size *= 2;
+    static std::atomic<unsigned long long> raised[2];  // one CTA, a cluster
     auto go = [&](auto kernel) {
-        cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Sm::kBytes);
+        const cudaError_t err = allow_smem(kernel, Sm::kBytes, raised[size > 1]);
         if (err != cudaSuccess) return err;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(rows * size));
