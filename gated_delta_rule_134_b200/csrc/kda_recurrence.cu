@@ -33,9 +33,8 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 256;
-constexpr int kGroups = kThreads / 8;  // token groups of a CTA (8 threads across the channels)
-constexpr int kMaxCluster = 8;
+constexpr int kTokens = 4;  // of a thread
+constexpr int kMaxCluster = 16;  // above 8 a device may refuse a cluster size: B200 takes 16
 
 // Token range of sequence n: the dense batch's [n T, (n + 1) T), or the packed
 // offsets clamped into [0, T] (a decreasing pair is an empty sequence).
@@ -120,7 +119,7 @@ __device__ __forceinline__ Pack<T> read_row(const T* row, int c0, int col, int D
 // __syncwarp). Words are swizzled by token group, so that the four groups of a warp read different banks. Rows that
 // begin in the middle of a word (ALIGN 2, every other row) are copied from that word on, 33 words, and shifted by the
 // reader; a word that reaches past the tensor's end `stop` is read by halves.
-template <typename T, int ALIGN, int R>
+template <typename T, int ALIGN, int R, int THREADS>
 __device__ __forceinline__ void copy_tile(uint32_t* slot, const T* first, int step, int left, int c0, int D, const T* stop) {
     constexpr int P = 4 / sizeof(T);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = lane & 7;
@@ -128,7 +127,7 @@ __device__ __forceinline__ void copy_tile(uint32_t* slot, const T* first, int st
         const int k0 = (threadIdx.x >> 3) * R, c = c0 + col * Pack<T>::V;
 #pragma unroll
         for (int i = 0; i < R; ++i)
-            cp_async16(reinterpret_cast<uint4*>(slot) + i * kThreads + threadIdx.x, first + (long long)(k0 + i) * step + c,
+            cp_async16(reinterpret_cast<uint4*>(slot) + i * THREADS + threadIdx.x, first + (long long)(k0 + i) * step + c,
                        k0 + i < left && c < D);
         return;
     }
@@ -153,7 +152,7 @@ __device__ __forceinline__ void copy_tile(uint32_t* slot, const T* first, int st
             if (lane < 4 * R && (reinterpret_cast<uintptr_t>(mine) & 2)) {
                 const char* w = mine - 2 + 128;
                 const bool on = lane < left && n == 64;
-                uint32_t* dst = slot + kGroups * R * 32 + k0 + lane;
+                uint32_t* dst = slot + THREADS / 8 * R * 32 + k0 + lane;
                 if (on && w + 4 > reinterpret_cast<const char*>(stop)) *dst = *reinterpret_cast<const unsigned short*>(w);
                 else cp_async4(dst, w, on);
             }
@@ -179,8 +178,8 @@ __device__ __forceinline__ void copy_tile(uint32_t* slot, const T* first, int st
     }
 }
 // This thread's channels of its token i; `odd`: the row begins in the middle of a word.
-template <typename T, int ALIGN, int R> __device__ __forceinline__ Pack<T> slot_of(const uint32_t* slot, int i, bool odd) {
-    if constexpr (ALIGN == 16) return Pack<T>::of(reinterpret_cast<const uint4*>(slot)[i * kThreads + threadIdx.x]);
+template <typename T, int ALIGN, int R, int THREADS> __device__ __forceinline__ Pack<T> slot_of(const uint32_t* slot, int i, bool odd) {
+    if constexpr (ALIGN == 16) return Pack<T>::of(reinterpret_cast<const uint4*>(slot)[i * THREADS + threadIdx.x]);
     const int col = threadIdx.x & 7, group = threadIdx.x >> 3, turn = 8 * (group & 3);
     const uint32_t* at = slot + (group * R + i) * 32;
     Pack<T> r;
@@ -189,7 +188,7 @@ template <typename T, int ALIGN, int R> __device__ __forceinline__ Pack<T> slot_
         const int k = col + 8 * j;
         r.w[j] = at[k ^ turn];
         if constexpr (ALIGN == 2) {
-            if (odd) r.w[j] = __funnelshift_r(r.w[j], k == 31 ? slot[kGroups * R * 32 + group * R + i] : at[(k + 1) ^ turn], 16);
+            if (odd) r.w[j] = __funnelshift_r(r.w[j], k == 31 ? slot[THREADS / 8 * R * 32 + group * R + i] : at[(k + 1) ^ turn], 16);
         }
     }
     return r;
@@ -229,10 +228,11 @@ __device__ __forceinline__ void store_row(T* row, int c0, int col, int D, const 
 
 // Shared memory: the ring of stages, the spans of the token groups, the states that enter them, and the spans of the
 // parts of all CTAs of the cluster, by parity of the tile.
-template <typename T, int R> struct ScanSmem {
+template <typename T, int R, int THREADS> struct ScanSmem {
+    static constexpr int kGroups = THREADS / 8;             // token groups of a CTA (8 threads across the channels)
     static constexpr int CT = 8 * Pack<T>::V;              // channels of a slice
-    static constexpr int kParts = kThreads / CT, kPer = kGroups / kParts;
-    static constexpr int kSlot = R * kThreads * 16 + kGroups * R * 4;  // one tensor's tile, and a word more a token
+    static constexpr int kParts = THREADS / CT, kPer = kGroups / kParts;
+    static constexpr int kSlot = R * THREADS * 16 + kGroups * R * 4;  // one tensor's tile, and a word more a token
     static constexpr int kStage = 2 * kSlot, kStages = 2;
     static constexpr int kSpans = kGroups * CT * (int)sizeof(float2), kStates = kGroups * CT * (int)sizeof(float);
     static constexpr int kBytes = kStages * kStage + kSpans + kStates + (kParts + 2) * CT * (int)sizeof(float2);
@@ -248,10 +248,10 @@ __device__ __forceinline__ void cluster_exchange() {
 }
 
 // R: tokens of a thread. CLUSTER: the cluster has more than one CTA.
-template <typename T, int ALIGN, bool BWD, int R, bool CLUSTER>
-__global__ void __launch_bounds__(kThreads, 2) recurrence_scan_kernel(RecurrenceArgs a, int slices) {
-    using Sm = ScanSmem<T, R>;
-    constexpr int V = Pack<T>::V, CT = Sm::CT, TILE = kGroups * R, PARTS = Sm::kParts, PER = Sm::kPer, S = Sm::kStages;
+template <typename T, int ALIGN, bool BWD, int R, int THREADS, bool CLUSTER>
+__global__ void __launch_bounds__(THREADS, 512 / THREADS) recurrence_scan_kernel(RecurrenceArgs a, int slices) {
+    using Sm = ScanSmem<T, R, THREADS>;
+    constexpr int V = Pack<T>::V, CT = Sm::CT, TILE = Sm::kGroups * R, PARTS = Sm::kParts, PER = Sm::kPer, S = Sm::kStages;
     extern __shared__ __align__(16) unsigned char smem[];
     uint32_t* ring = reinterpret_cast<uint32_t*>(smem);
     float4* spans = reinterpret_cast<float4*>(smem + S * Sm::kStage);                  // [group][pair of V/2][col]: A, H, A, H
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_scan_kernel(Recurrence
 
     // token k of this CTA's tile `tile`, in walking order; -1: past the end
     auto token = [&](int tile, int k) {
-        const unsigned at = (unsigned)(tile * size + rank) * TILE + k;  // below len + 8 TILE: no wrap
+        const unsigned at = (unsigned)(tile * size + rank) * TILE + k;  // below len + 16 TILE: no wrap
         return at < (unsigned)len ? (BWD ? len - 1 - (int)at : (int)at) : -1;
     };
     constexpr int kSlot = Sm::kSlot / 4;
@@ -297,8 +297,8 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_scan_kernel(Recurrence
         const long long at = (long long)(tile * size + rank) * TILE;
         const int left = (int)min(max(len - at, 0ll), (long long)TILE);
         const long long row = (BWD ? len - 1 - at : at) * D;
-        copy_tile<T, ALIGN, R>(to, la + row, BWD ? -D : D, left, c0, D, la_stop);
-        copy_tile<T, ALIGN, R>(to + kSlot, x + row, BWD ? -D : D, left, c0, D, x_stop);
+        copy_tile<T, ALIGN, R, THREADS>(to, la + row, BWD ? -D : D, left, c0, D, la_stop);
+        copy_tile<T, ALIGN, R, THREADS>(to + kSlot, x + row, BWD ? -D : D, left, c0, D, x_stop);
     };
     const long long step = (long long)size * TILE;
     const int tiles = (int)((len + step - 1) / step);
@@ -327,8 +327,8 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_scan_kernel(Recurrence
                 // (those past the end, which hold zeros, counted on: the copy goes by the same rows)
                 const int at = (tile * size + rank) * TILE + group * R + i;
                 const bool odd = ALIGN == 2 && (((int)begin + (BWD ? len - 1 - at : at)) & 1);
-                const Pack<T> pl = slot_of<T, ALIGN, R>(from, i, odd);
-                px[i] = slot_of<T, ALIGN, R>(from + kSlot, i, odd);
+                const Pack<T> pl = slot_of<T, ALIGN, R, THREADS>(from, i, odd);
+                px[i] = slot_of<T, ALIGN, R, THREADS>(from + kSlot, i, odd);
 #pragma unroll
                 for (int e = 0; e < V / 2; ++e) {
                     d[i][e] = f2(decay<T>(pl.get(2 * e)), decay<T>(pl.get(2 * e + 1)));
@@ -375,16 +375,18 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_scan_kernel(Recurrence
             float2* mine = whole_of + (tile & 1) * CT + p;
             if (part == 0) *mine = whole;
             cluster_exchange();
-            float2 u[kMaxCluster];
+            for (int r0 = 0; r0 < size; r0 += 8) {
+                float2 u[8];
 #pragma unroll
-            for (int r = 0; r < kMaxCluster; ++r)
-                if (r < size) u[r] = *cg::this_cluster().map_shared_rank(mine, r);
+                for (int r = 0; r < 8; ++r)
+                    if (r0 + r < size) u[r] = *cg::this_cluster().map_shared_rank(mine, r0 + r);
 #pragma unroll
-            for (int r = 0; r < kMaxCluster; ++r)
-                if (r < size) {
-                    if (r == rank) s = state;
-                    state = fmaf(u[r].x, state, u[r].y);
-                }
+                for (int r = 0; r < 8; ++r)
+                    if (r0 + r < size) {
+                        if (r0 + r == rank) s = state;
+                        state = fmaf(u[r].x, state, u[r].y);
+                    }
+            }
         } else {
             state = fmaf(whole.x, state, whole.y);
         }
@@ -441,46 +443,88 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_scan_kernel(Recurrence
     if (part == 0 && rank == 0 && pc < D && a.state_end) a.state_end[(long long)n * D + pc] = state;
 }
 
+// One token: four cells a thread, 16 bytes of state (the tensors are contiguous, so their rows do not matter).
 template <typename T>
-__global__ void recurrence_step_kernel(const T* log_alpha, const T* x, const float* h_in, float* h_out, T* y,
-                                       long long cells) {
-    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-    if (i >= cells) return;
-    const float s = fmaf(expf(to_f32(log_alpha[i])), h_in[i], to_f32(x[i]));
-    h_out[i] = s;
-    y[i] = from_f32<T>(s);
+__global__ void __launch_bounds__(256) recurrence_step_kernel(const T* log_alpha, const T* x, const float* h_in, float* h_out, T* y,
+                                                              long long cells) {
+    const long long i = ((long long)blockIdx.x * blockDim.x + threadIdx.x) * 4;
+    if (i + 4 <= cells) {
+        float la[4], v[4];
+        if constexpr (sizeof(T) == 4) {
+            const float4 l4 = *reinterpret_cast<const float4*>(log_alpha + i), x4 = *reinterpret_cast<const float4*>(x + i);
+            la[0] = l4.x; la[1] = l4.y; la[2] = l4.z; la[3] = l4.w;
+            v[0] = x4.x; v[1] = x4.y; v[2] = x4.z; v[3] = x4.w;
+        } else {
+            const uint2 l2 = *reinterpret_cast<const uint2*>(log_alpha + i), x2 = *reinterpret_cast<const uint2*>(x + i);
+            const uint32_t l[2] = {l2.x, l2.y}, w[2] = {x2.x, x2.y};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                la[e] = __uint_as_float(e & 1 ? l[e >> 1] & 0xffff0000u : l[e >> 1] << 16);
+                v[e] = __uint_as_float(e & 1 ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16);
+            }
+        }
+        const float4 h = *reinterpret_cast<const float4*>(h_in + i);
+        const float4 s = make_float4(fmaf(expf(la[0]), h.x, v[0]), fmaf(expf(la[1]), h.y, v[1]), fmaf(expf(la[2]), h.z, v[2]),
+                                     fmaf(expf(la[3]), h.w, v[3]));
+        *reinterpret_cast<float4*>(h_out + i) = s;
+        if constexpr (sizeof(T) == 4) {
+            *reinterpret_cast<float4*>(y + i) = s;
+        } else {
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(s.x, s.y), hi = __floats2bfloat162_rn(s.z, s.w);
+            *reinterpret_cast<uint2*>(y + i) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+        }
+        return;
+    }
+    for (long long k = i; k < cells; ++k) {
+        const float s = fmaf(expf(to_f32(log_alpha[k])), h_in[k], to_f32(x[k]));
+        h_out[k] = s;
+        y[k] = from_f32<T>(s);
+    }
+}
+
+template <typename T, int ALIGN, bool BWD, int THREADS, bool CLUSTER>
+cudaError_t launch_scan_as(const RecurrenceArgs& a, int slices, int size, cudaStream_t stream) {
+    using Sm = ScanSmem<T, kTokens, THREADS>;
+    auto kernel = recurrence_scan_kernel<T, ALIGN, BWD, kTokens, THREADS, CLUSTER>;
+    static std::atomic<unsigned long long> raised{0};
+    cudaError_t err = size > 8 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) : cudaSuccess;
+    if (err == cudaSuccess) err = allow_smem(kernel, Sm::kBytes, raised);
+    if (err != cudaSuccess) return err;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((long long)a.N * slices * size));
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = Sm::kBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = size;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = CLUSTER ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, a, slices);
 }
 
 template <typename T, int ALIGN, bool BWD>
 cudaError_t launch_scan(const RecurrenceArgs& a, cudaStream_t stream) {
-    constexpr int R = 4;
-    using Sm = ScanSmem<T, R>;
-    const int slices = (a.D + Sm::CT - 1) / Sm::CT;
+    constexpr int CT = 8 * Pack<T>::V;
+    const int slices = (a.D + CT - 1) / CT;
     const long long rows = (long long)a.N * slices;
-    // CTAs of a cluster: one where that nearly fills the SMs (128 rows, T 8192, D 4096 backward: 127 us, with two 131);
-    // else as many as fill two CTAs on each SM (64 rows, T 4096: 24 us with four, 31 with two, 40 with one), no more than
-    // the tokens give tiles to.
     const long long tokens = a.cu_seqlens ? (a.T + a.N - 1) / a.N : a.T;
+    // CTAs of a cluster: one from 75 rows on (128 rows, T 8192 backward: 127 us, with two 131; 96 rows, T 4096: 36 and
+    // 44); below, as many as fill two CTAs on each SM, so that one computes while the other exchanges (64 rows, T 4096:
+    // 24 us with four, 31 with two, 40 with one), no more than the tokens give tiles to; sixteen only where all clusters
+    // of them fit at once (T 16384: six rows 27 us, with eight 34; eight rows 37 and 34).
     int size = 1;
-    while (rows < 128 && size < kMaxCluster && rows * size * 2 <= 2 * 148 && (long long)size * kGroups * R < tokens) size *= 2;
-    static std::atomic<unsigned long long> raised[2];  // one CTA, a cluster
-    auto go = [&](auto kernel) {
-        const cudaError_t err = allow_smem(kernel, Sm::kBytes, raised[size > 1]);
-        if (err != cudaSuccess) return err;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)(rows * size));
-        cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = Sm::kBytes;
-        cfg.stream = stream;
-        cudaLaunchAttribute attr;
-        attr.id = cudaLaunchAttributeClusterDimension;
-        attr.val.clusterDim.x = size;
-        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-        cfg.attrs = &attr;
-        cfg.numAttrs = size > 1 ? 1 : 0;
-        return cudaLaunchKernelEx(&cfg, kernel, a, slices);
-    };
-    return size > 1 ? go(recurrence_scan_kernel<T, ALIGN, BWD, R, true>) : go(recurrence_scan_kernel<T, ALIGN, BWD, R, false>);
+    while (rows < 75 && size < (rows <= 6 ? kMaxCluster : 8) && rows * size * 2 <= 2 * 148 &&
+           (long long)size * (256 / 8) * kTokens < tokens)
+        size *= 2;
+    if (size > 1) return launch_scan_as<T, ALIGN, BWD, 256, true>(a, slices, size, stream);
+    // One CTA of 512 threads on an SM takes tiles of twice the tokens, and its SM's share of the bandwidth with fewer
+    // barriers: 256 rows, T 8192 132 us (two CTAs of 256 threads: 150); 96 rows, T 4096 backward 51 (65). It pays where
+    // the rows fill their rounds of 148 (192 rows: 67 us against 57) and there are tokens enough (T 200: 7.4 against 5.8).
+    const long long rounds = (rows + 147) / 148;
+    if (tokens >= 512 && (rounds == 1 || rows * 5 >= rounds * 148 * 4)) return launch_scan_as<T, ALIGN, BWD, 512, false>(a, slices, 1, stream);
+    return launch_scan_as<T, ALIGN, BWD, 256, false>(a, slices, 1, stream);
 }
 
 template <bool BWD> cudaError_t launch_scan_any(const RecurrenceArgs& a, cudaStream_t stream) {
@@ -501,8 +545,10 @@ cudaError_t launch_recurrence_step(const void* la, const void* x, const float* h
                                    long long cells, int bf16, cudaStream_t stream) {
     auto go = [&](auto t) {
         using T = decltype(t);
-        recurrence_step_kernel<T><<<(unsigned)((cells + 127) / 128), 128, 0, stream>>>((const T*)la, (const T*)x, h_in, h_out,
-                                                                                      (T*)y, cells);
+        // 64 threads a block for few cells, so that they meet all SMs
+        const int threads = cells < 148ll * 1024 ? 64 : 256;
+        const long long blocks = (cells + threads * 4 - 1) / (threads * 4);
+        recurrence_step_kernel<T><<<(unsigned)blocks, threads, 0, stream>>>((const T*)la, (const T*)x, h_in, h_out, (T*)y, cells);
         return cudaGetLastError();
     };
     return bf16 ? go(__nv_bfloat16()) : go(float());
