@@ -150,6 +150,19 @@ def test_infinite_keys(cuda_lib):
         R.close(o[:1], want, 4 * calm)  # the finite keys set the scores' error
 
 
+def test_infinite_values(cuda_lib):
+    """An attended infinity comes out as one where its weight is positive, and stays in its channel."""
+    for dtype in ("f32", "bf16"):
+        s = make([40], 4, 2, 64, 16, dtype, 23)
+        s["vc"][int(s["table"][0, 1]), 0, 5, 7] = math.inf
+        s["vc"][int(s["table"][0, 1]), 1, 5, 9] = -math.inf
+        c = {n: t.cuda() for n, t in s.items()}
+        o = cuda_lib.attn_decode(c["q"], c["kc"], c["vc"], c["table"], c["lens"], k=c["k"], v=c["v"])
+        assert (o[0, :2, 7] == math.inf).all() and (o[0, 2:, 9] == -math.inf).all()
+        o[0, :2, 7] = o[0, 2:, 9] = 0
+        assert torch.isfinite(o).all()
+
+
 def test_decode_loop_fills_the_cache(cuda_lib):
     """From an empty cache, token by token: each step equals attention over what came before."""
     N, Hq, Hk, d, page, steps = 3, 8, 2, 64, 16, 40
