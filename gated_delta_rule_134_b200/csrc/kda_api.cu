@@ -405,6 +405,9 @@ kda_status_t kda_attn_decode(const void* q, const void* k_new, const void* v_new
     // so are the rows of a cache (one of more would not fit the device)
     if ((long long)n_pages * page_size > 0x7fffffffLL || (long long)n_pages * page_size * Hk > 0x7fffffffLL)
         return KDA_ERR_INVALID_ARG;
+    // a worker's share of the work (one of 592 at least) is counted in int32: reached only by capacities that no run ends
+    const long long tiles = (long long)max_pages * page_size / 16 + 4, pairs = (long long)N * Hk * ((Hq / Hk + 15) / 16);
+    if (pairs > 0 && tiles > 0x7fffffffLL * 512 / pairs) return KDA_ERR_INVALID_ARG;
     if (N == 0) return KDA_OK;
     if (!good(q) || !good(o)) return KDA_ERR_INVALID_ARG;
     if ((k_new == nullptr) != (v_new == nullptr)) return KDA_ERR_INVALID_ARG;

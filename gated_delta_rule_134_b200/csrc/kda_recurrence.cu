@@ -325,8 +325,8 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) recurrence_scan_kernel
             for (int i = 0; i < R; ++i) {
                 // D is odd and the tensors begin on 16 bytes: every other row begins in the middle of a word
                 // (those past the end, which hold zeros, counted on: the copy goes by the same rows)
-                const int at = (tile * size + rank) * TILE + group * R + i;
-                const bool odd = ALIGN == 2 && (((int)begin + (BWD ? len - 1 - at : at)) & 1);
+                const unsigned at = (unsigned)(tile * size + rank) * TILE + group * R + i;
+                const bool odd = ALIGN == 2 && (((unsigned)begin + (BWD ? len - 1 - at : at)) & 1);
                 const Pack<T> pl = slot_of<T, ALIGN, R, THREADS>(from, i, odd);
                 px[i] = slot_of<T, ALIGN, R, THREADS>(from + kSlot, i, odd);
 #pragma unroll

@@ -339,8 +339,11 @@ kda_status_t kda_noalloc_status(void *stream);
  *
  *     h_t = exp(log_alpha_t) * h_{t-1} + x_t
  *
- *   log_alpha, x    : [N, T, D]       dtype (no activation is applied; meant
- *                                     to be <= 0, -INFINITY resets a channel)
+ *   log_alpha, x    : [N, T, D]       dtype (no activation is applied).
+ *                                     log_alpha is meant to be <= 0; -INFINITY
+ *                                     resets a channel. With positive values
+ *                                     the decays' products over spans of up to
+ *                                     4096 tokens have to stay finite
  *   h0              : [N, D]          float, initial state; NULL means zero
  *   h               : [N, T, D]       dtype, written (may equal x)
  *   h_T             : [N, D]          float, final state before its rounding
@@ -433,7 +436,8 @@ kda_status_t kda_qk_norm_rope(const void *q, const void *k, const void *q_weight
  * and heads, in a fixed order; NULL: not computed (the workspace is then not
  * used and may be NULL).
  *   workspace       : device scratch, 16-byte aligned, of
- *                     kda_qk_norm_rope_bwd_workspace_size(...) bytes
+ *                     kda_qk_norm_rope_bwd_workspace_size(...) bytes; two calls
+ *                     in flight at once must not share one
  */
 size_t kda_qk_norm_rope_bwd_workspace_size(int n, int Hq, int Hk, int d);
 kda_status_t kda_qk_norm_rope_bwd(const void *d_q_out, const void *d_k_out, const void *q, const void *k,
@@ -471,7 +475,9 @@ kda_status_t kda_qk_norm_rope_bwd(const void *d_q_out, const void *d_k_out, cons
  *                     two calls in flight at once must not share one
  * page_table and seq_lens are read on the device only: positions past
  * max_pages * page_size, and positions on pages outside [0, n_pages), are not
- * attended, and a new token with such a position is not put in. A row without
+ * attended, and a new token with such a position is not put in. max_pages *
+ * page_size must stay below 2^30, n_pages * Hk * page_size and N * Hq below 2^31
+ * and 2^24. A row without
  * any attended position gives o = 0 and lse = -INFINITY. Rows of a page behind
  * its sequence's last position are never read into a sum (they may hold NaN).
  * The page that takes a new token must belong to its sequence alone.

@@ -90,7 +90,7 @@ def attn(q=P[0], k=P[1], v=P[2], kc=P[3], vc=P[4], table=P[5], lens=P[6], o=P[7]
     (dict(q=None), 1), (dict(q=ODD), 1), (dict(k=None), 1), (dict(v=None), 1), (dict(k=ODD), 1), (dict(v=ODD), 1), (dict(kc=None), 1), (dict(vc=ODD), 1),
     (dict(table=None), 1), (dict(table=HALF), 1), (dict(lens=None), 1), (dict(lens=HALF), 1), (dict(o=None), 1), (dict(o=ODD), 1), (dict(lse=HALF), 1),
     (dict(N=-1), 1), (dict(Hq=3), 1), (dict(Hq=0), 1), (dict(Hk=0), 1), (dict(Hk=-2), 1), (dict(d=96), 2), (dict(d=256), 2), (dict(pages=-1), 1), (dict(page=0), 1),
-    (dict(most=-1), 1), (dict(most=1 << 28, page=16), 1), (dict(N=1 << 28), 1), (dict(window=-1), 1), (dict(scale=math.nan), 1), (dict(dtype=2), 1)])
+    (dict(most=-1), 1), (dict(most=1 << 28, page=16), 1), (dict(N=1 << 28), 1), (dict(N=1 << 21, most=1 << 25, page=16), 1), (dict(pages=1 << 30, page=2), 1), (dict(pages=1 << 26, page=16), 1), (dict(window=-1), 1), (dict(scale=math.nan), 1), (dict(dtype=2), 1)])
 def test_attn_refuses(bad, status):
     assert attn(**bad) == status
 
