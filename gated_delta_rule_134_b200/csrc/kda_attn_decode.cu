@@ -628,14 +628,15 @@ __global__ void __launch_bounds__(kWarps * 32, Plan<T, D>::kCtasPerSm) attn_spli
 
 // Joins the pieces of every (pair, query head) that lies in several workers, in
 // their order: piece 0 in place 1 of the worker that begins the pair, the others
-// in place 0 of the workers after it. WARPS warps share the pieces: 8 where
-// there are few pairs, so many pieces of each, 1 where there are many. A warp
-// loads up to four pieces at once, maxima and sums with them, so that the chain
-// of dependent loads is two long.
-constexpr int kJoinWarps = 8;
+// in place 0 of the workers after it. WARPS warps share the pieces: 32 or 8
+// where there are few pairs, so many pieces of each (one pair of 1184 pieces: 36
+// us a call with 8, 22 with 32), 1 where there are many. A warp loads up to four
+// pieces at once, maxima and sums with them, so that the chain of dependent
+// loads is two long.
+constexpr int kJoinWarps = 8;  // of a block, where a warp works alone
 
 template <typename T, int D, int WARPS>
-__global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(AttnDecodeArgs a, int items) {
+__global__ void __launch_bounds__((WARPS == 1 ? kJoinWarps : WARPS) * 32) attn_join_kernel(AttnDecodeArgs a, int items) {
     constexpr int E = D / 32, B = 4;
     __shared__ float so[WARPS == 1 ? 1 : WARPS][D];
     __shared__ float2 sml[WARPS];
@@ -697,18 +698,15 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(AttnDecodeAr
         __syncthreads();
         ref = -INFINITY;
         sum = 0.f;
-        float f[WARPS];
 #pragma unroll
         for (int w = 0; w < WARPS; ++w) ref = fmaxf(ref, sml[w].x);
+        auto factor = [&](int w) { return sml[w].x == -INFINITY ? 0.f : exp2_fast(sml[w].x - ref); };
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) {
-            f[w] = sml[w].x == -INFINITY ? 0.f : exp2_fast(sml[w].x - ref);
-            sum = fmaf(sml[w].y, f[w], sum);
-        }
+        for (int w = 0; w < WARPS; ++w) sum = fmaf(sml[w].y, factor(w), sum);
         for (int c = threadIdx.x; c < D; c += WARPS * 32) {
             float x = 0.f;
 #pragma unroll
-            for (int w = 0; w < WARPS; ++w) x = fmaf(so[w][c], f[w], x);
+            for (int w = 0; w < WARPS; ++w) x = fmaf(so[w][c], factor(w), x);
             ((T*)a.o)[out * D + c] = from_f32<T>(sum == 0.f ? 0.f : x / sum);
         }
     }
@@ -736,18 +734,18 @@ static cudaError_t launch_attn(const AttnDecodeArgs& a, cudaStream_t stream) {
     split<<<Geo::kCtas, kWarps * 32, Geo::kSmem, stream>>>(a);
     if ((err = cudaGetLastError()) != cudaSuccess) return err;
     // The join is launched while the split kernel runs (programmatic dependent launch) and waits for its end.
-    const bool few = pairs < 148;
+    const int warps = pairs < 16 ? 32 : pairs < 148 ? 8 : 1;
     const int items = pairs * (G < kHeads ? G : kHeads);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(few ? items : (items + kJoinWarps - 1) / kJoinWarps);
-    cfg.blockDim = dim3(kJoinWarps * 32);
+    cfg.gridDim = dim3(warps > 1 ? items : (items + kJoinWarps - 1) / kJoinWarps);
+    cfg.blockDim = dim3(32 * (warps > 1 ? warps : kJoinWarps));
     cfg.stream = stream;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, few ? attn_join_kernel<T, D, kJoinWarps> : attn_join_kernel<T, D, 1>, a, items);
+    return cudaLaunchKernelEx(&cfg, warps == 32 ? attn_join_kernel<T, D, 32> : warps == 8 ? attn_join_kernel<T, D, 8> : attn_join_kernel<T, D, 1>, a, items);
 }
 
 template <typename T, int D>
