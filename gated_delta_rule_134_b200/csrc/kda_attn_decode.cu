@@ -32,21 +32,21 @@ namespace {
 
 constexpr int kTile = 16;   // positions of a tile
 constexpr int kHeads = 16;  // query heads of a block
-constexpr int kWarps = 4;   // workers of a CTA
 constexpr int kBegin = 3;   // what a pair costs beside its tiles, in tiles
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// Stages of a worker's ring and CTAs of an SM: about 190 KB of cache rows in
-// flight an SM, by as many warps as the registers allow.
+// Stages of a worker's ring, workers of a CTA and CTAs of an SM: 190 to 220 KB
+// of cache rows an SM, by as many warps as the registers allow.
 template <typename T, int D> struct Plan;
-template <> struct Plan<__nv_bfloat16, 128> { static constexpr int kStages = 3, kCtasPerSm = 2; };
-template <> struct Plan<__nv_bfloat16, 64> { static constexpr int kStages = 4, kCtasPerSm = 3; };
-template <> struct Plan<float, 128> { static constexpr int kStages = 3, kCtasPerSm = 1; };
-template <> struct Plan<float, 64> { static constexpr int kStages = 3, kCtasPerSm = 2; };
+template <> struct Plan<__nv_bfloat16, 128> { static constexpr int kStages = 3, kWarps = 4, kCtasPerSm = 2; };
+template <> struct Plan<__nv_bfloat16, 64> { static constexpr int kStages = 4, kWarps = 4, kCtasPerSm = 3; };
+template <> struct Plan<float, 128> { static constexpr int kStages = 2, kWarps = 7, kCtasPerSm = 1; };
+template <> struct Plan<float, 64> { static constexpr int kStages = 2, kWarps = 6, kCtasPerSm = 2; };
 
 template <typename T, int D> struct Geometry : Plan<T, D> {
     static constexpr int kRowBytes = D * (int)sizeof(T), kChunks = kRowBytes / 16;
     static constexpr int kStageBytes = 2 * kTile * kRowBytes;  // K then V
+    using Plan<T, D>::kWarps;
     static constexpr int kCtas = 148 * Plan<T, D>::kCtasPerSm, kWorkers = kCtas * kWarps;
     static constexpr int kSmem = kWarps * Plan<T, D>::kStages * (kStageBytes + 16);
 };
@@ -127,13 +127,13 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], 
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// x = hi + lo + at most 2^-22 |x|, each part a tf32 number. An infinity goes into
-// lo alone: products with the other operand's hi then have its sign, and there
+// x = hi + lo: hi is x rounded to tf32's 11 significant bits, lo the rest. The MMA ignores lo's bits past its own 11,
+// 2^-22 |x| at most. An infinity goes into lo alone: products with the other operand's hi then have its sign, and there
 // is no infinity times a part that happens to be zero.
 __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
+    hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
     if (!(fabsf(x) < INFINITY)) hi = 0u;
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(x - __uint_as_float(hi)));
+    lo = __float_as_uint(x - __uint_as_float(hi));
 }
 __device__ __forceinline__ float lds_f32(uint32_t at) {
     float x;
@@ -312,7 +312,7 @@ struct Feed {
 // Rows without any attended position get their zeros here.
 template <typename T, int D>
 __device__ __forceinline__ bool find_range(const AttnDecodeArgs& a, const Pieces& ws, long long& W, int& count, int& row, long long& rem) {
-    constexpr int kWorkers = Geometry<T, D>::kWorkers, CH = Geometry<T, D>::kChunks;
+    constexpr int kWorkers = Geometry<T, D>::kWorkers, CH = Geometry<T, D>::kChunks, kWarps = Geometry<T, D>::kWarps;
     __shared__ long long s_part[kWarps], s_rem[kWarps];
     __shared__ int s_row[kWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -370,16 +370,17 @@ __device__ __forceinline__ bool find_range(const AttnDecodeArgs& a, const Pieces
 //     S^T [16 x 8 NT] = K Q^T,  O^T [D x 8 NT] += V^T P^T.
 // bf16 operands go in as they are, the weights rounded to bf16. 32-bit operands
 // are split into two tf32 parts each, and three products taken (the fourth,
-// lo * lo, is below 2^-22 of the whole), which keeps 32-bit accuracy at a quarter
-// of the instructions that multiply-adds would take.
+// lo * lo, is below 2^-22 of the whole), which keeps 32-bit accuracy. The split
+// is integer rounding and a subtraction: with the conversion instruction in its
+// place 64 rows of 1000 positions took 169 us, now 95.
 // The weights' maximum is a reference that moves only when a score passes it by
 // more than 2^8: until then weights reach 2^8, far from any overflow in 32
 // bits, and neither a reduction over the warp nor a rescaling is due.
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kWarps * 32, Plan<T, D>::kCtasPerSm) attn_split_kernel(AttnDecodeArgs a) {
+__global__ void __launch_bounds__(Plan<T, D>::kWarps * 32, Plan<T, D>::kCtasPerSm) attn_split_kernel(AttnDecodeArgs a) {
     using Geo = Geometry<T, D>;
     constexpr bool BF = sizeof(T) == 2;
-    constexpr int S = Geo::kStages, RB = Geo::kRowBytes;
+    constexpr int S = Geo::kStages, RB = Geo::kRowBytes, kWarps = Geo::kWarps;
     constexpr int KS = BF ? D / 16 : D / 8;  // steps of the K Q^T product
     constexpr bool SPLIT_Q = !BF && NT == 1;  // both tf32 parts of the queries kept (16 heads: split anew each time)
     constexpr float kSlackLog2 = 8.f;
@@ -548,16 +549,16 @@ __global__ void __launch_bounds__(kWarps * 32, Plan<T, D>::kCtasPerSm) attn_spli
                         const float x0 = __shfl_sync(~0u, s[j][2 * b], src), x1 = __shfl_sync(~0u, s[j][2 * b + 1], src);
                         split_tf32(g & 1 ? x1 : x0, ph[b][j][e], pl[b][j][e]);
                     }
+            const uint32_t v0 = vt + c2 * RB + (((g >> 2) ^ c2) << 4) + (g & 3) * 4;              // channel g of position 2 c
+            const uint32_t v1 = vt + (c2 + 1) * RB + (((g >> 2) ^ (c2 + 1)) << 4) + (g & 3) * 4;  // of 2 c + 1
 #pragma unroll
             for (int i = 0; i < D / 16; ++i)
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
                     uint32_t hi[4], lo[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {  // elements 0, 1: channels g, g + 8 of position 2 c; 2, 3: of 2 c + 1
-                        const int r = b * 8 + c2 + (e >> 1), ch = i * 4 + (e & 1) * 2 + (g >> 2);
-                        split_tf32(lds_f32(vt + r * RB + ((ch ^ (r & 7)) << 4) + (g & 3) * 4), hi[e], lo[e]);
-                    }
+                    for (int e = 0; e < 4; ++e)  // elements 0, 1: channels 16 i + g, + 8 of position 2 c; 2, 3: of 2 c + 1
+                        split_tf32(lds_f32(((e >> 1 ? v1 : v0) ^ ((i & 1) * 64 + (e & 1) * 32)) + b * 8 * RB + (i >> 1) * 128), hi[e], lo[e]);
 #pragma unroll
                     for (int j = 0; j < NT; ++j) {
                         mma_tf32(o[i][j], lo, ph[b][j][0], ph[b][j][1]);
@@ -731,7 +732,7 @@ static cudaError_t launch_attn(const AttnDecodeArgs& a, cudaStream_t stream) {
     static std::atomic<unsigned long long> raised{0};
     cudaError_t err = allow_smem(split, Geo::kSmem, raised);
     if (err != cudaSuccess) return err;
-    split<<<Geo::kCtas, kWarps * 32, Geo::kSmem, stream>>>(a);
+    split<<<Geo::kCtas, Geo::kWarps * 32, Geo::kSmem, stream>>>(a);
     if ((err = cudaGetLastError()) != cudaSuccess) return err;
     // The join is launched while the split kernel runs (programmatic dependent launch) and waits for its end.
     const int warps = pairs < 16 ? 32 : pairs < 148 ? 8 : 1;
