@@ -22,6 +22,7 @@
 // pair and does not end it. attn_join_kernel joins the pieces in order. A warp
 // works for itself (no block barrier in the loop): it copies 16 rows of K and V
 // a stage with 16-byte cp.async, several stages ahead, across the ends of pairs.
+#include "kda_async.cuh"
 #include "kda_common.cuh"
 #include "kda_internal.h"
 #include "kda_sm100.cuh"

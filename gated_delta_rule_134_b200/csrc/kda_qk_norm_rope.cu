@@ -15,6 +15,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "kda_async.cuh"
 #include "kda_common.cuh"
 #include "kda_internal.h"
 

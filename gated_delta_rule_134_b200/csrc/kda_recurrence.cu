@@ -22,6 +22,7 @@
 //   4. runs its tokens again from the state that enters them and writes them.
 // The sequential depth is T / (tokens of a cluster's tile). Nothing waits on a
 // flag, and the order of every product and sum is fixed by the sizes alone.
+#include "kda_async.cuh"
 #include "kda_common.cuh"
 #include "kda_internal.h"
 
