@@ -16,7 +16,7 @@ import os
 
 __all__ = ["load", "chunk_fwd", "chunk_fwd_varlen", "chunk_bwd", "chunk_fwd_noalloc", "noalloc_status", "decode_step",
            "workspace_size", "workspace_status", "chunk_fwd_timeout_test", "KDAError", "library_path", "STATUS",
-           "recurrence_fwd", "recurrence_bwd", "recurrence_step", "qk_norm_rope", "qk_norm_rope_bwd", "attn_decode",
+           "recurrence_fwd", "recurrence_bwd", "recurrence_step", "recurrence_status", "recurrence_timeout_test", "qk_norm_rope", "qk_norm_rope_bwd", "attn_decode",
            "attn_decode_workspace_size"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -96,6 +96,10 @@ def load(build_if_stale: bool = True):
     lib.kda_recurrence_fwd.restype = I
     lib.kda_recurrence_bwd.argtypes = [P] * 9 + [I] * 4 + [P]
     lib.kda_recurrence_bwd.restype = I
+    lib.kda_recurrence_status.argtypes = [P]
+    lib.kda_recurrence_status.restype = I
+    lib.kda_recurrence_timeout_test.argtypes = [P] * 3 + [I] * 4 + [L, P]
+    lib.kda_recurrence_timeout_test.restype = I
     lib.kda_recurrence_step.argtypes = [P] * 5 + [I] * 3 + [P]
     lib.kda_recurrence_step.restype = I
     lib.kda_qk_norm_rope.argtypes = [P] * 7 + [I] + [P] * 2 + [I] * 6 + [L] * 4 + [I, F, F, I, I, P]
@@ -546,6 +550,32 @@ def recurrence_step(log_alpha, x, h, *, h_out=None, y=None, stream=None):
                                        _stream(stream, dev))
     _check("kda_recurrence_step", code)
     return y, h_out
+
+
+def recurrence_status(device=None, stream=None) -> int:
+    """kda_recurrence_status: synchronise and return whether a wait inside a
+    recurrence_fwd or recurrence_bwd on `device` gave up since this was last
+    asked (0 = KDA_OK, 4 = KDA_ERR_TIMEOUT: those outputs are invalid)."""
+    import torch
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    with _on(dev):
+        return int(load().kda_recurrence_status(_stream(stream, dev)))
+
+
+def recurrence_timeout_test(log_alpha, x, *, h, wait_budget_cycles: int, stream=None):
+    """kda_recurrence_timeout_test: recurrence_fwd with the first CTA of every
+    cluster sending nothing and every wait bounded by wait_budget_cycles SM
+    cycles, so that the waits give up (read recurrence_status). A test hook; h
+    is left undefined."""
+    lib = load()
+    N, T, D = _recurrence_sizes(log_alpha, None)
+    dt, dev = log_alpha.dtype, log_alpha.device
+    for t, name in ((log_alpha, "log_alpha"), (x, "x"), (h, "h")):
+        _need(t, name, (N, T, D), dt, dev)
+    with _on(dev):
+        code = lib.kda_recurrence_timeout_test(_ptr(log_alpha), _ptr(x), _ptr(h), N, T, D, _DTYPE[_dtype_of(x)],
+                                               int(wait_budget_cycles), _stream(stream, dev))
+    _check("kda_recurrence_timeout_test", code)
 
 
 # ---------------------------------------------------------------- query/key norm and rotation

@@ -281,6 +281,28 @@ kda_status_t kda_recurrence_fwd(const void* log_alpha, const void* x, const floa
     return kda::launch_recurrence_fwd(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
+kda_status_t kda_recurrence_timeout_test(const void* log_alpha, const void* x, void* h, int N, int T, int D,
+                                         kda_dtype_t dtype, long long wait_budget_cycles, void* stream) {
+    if (wait_budget_cycles <= 0 || wait_budget_cycles > (1ll << 31)) return KDA_ERR_INVALID_ARG;
+    kda::RecurrenceArgs a{};
+    a.log_alpha = log_alpha; a.x = x; a.out = h;
+    a.N = N; a.T = T; a.D = D; a.bf16 = dtype == KDA_BF16;
+    a.wait_cycles = wait_budget_cycles;
+    a.test_withhold = 1;
+    const kda_status_t st = check_recurrence(a, dtype, false);
+    if (st != KDA_OK) return st;
+    // Only a cluster waits: a few rows of at least 512 tokens.
+    if (N < 1 || T < 512 || (long long)N * ((D + 31) / 32) >= 75) return KDA_ERR_INVALID_ARG;
+    return kda::launch_recurrence_fwd(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+kda_status_t kda_recurrence_status(void* stream) {
+    if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return KDA_ERR_CUDA;
+    unsigned flag = 0;
+    if (kda::recurrence_late(&flag) != cudaSuccess) return KDA_ERR_CUDA;
+    return flag ? KDA_ERR_TIMEOUT : KDA_OK;
+}
+
 kda_status_t kda_recurrence_bwd(const void* log_alpha, const void* h, const float* h0, const void* d_h,
                                 const float* d_h_T, void* d_x, void* d_log_alpha, float* d_h0,
                                 const int* cu_seqlens, int N, int T, int D, kda_dtype_t dtype, void* stream) {

@@ -90,7 +90,11 @@ struct RecurrenceArgs {
     float* state_end;           // forward: h_T; backward: d_h0
     const int* cu_seqlens;
     int N, T, D, bf16;
+    long long wait_cycles = 1ll << 31;  // SM cycles that a wait within a cluster lasts at most: about a second
+    int test_withhold = 0;              // fault injection: the first CTA of a cluster sends nothing
 };
+// Whether a wait gave up on the current device since the last call; clears it.
+cudaError_t recurrence_late(unsigned* flag);
 cudaError_t launch_recurrence_fwd(const RecurrenceArgs& a, cudaStream_t stream);
 cudaError_t launch_recurrence_bwd(const RecurrenceArgs& a, cudaStream_t stream);
 cudaError_t launch_recurrence_step(const void* la, const void* x, const float* h_in, float* h_out, void* y,

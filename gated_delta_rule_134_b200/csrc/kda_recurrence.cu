@@ -25,6 +25,7 @@
 #include "kda_async.cuh"
 #include "kda_common.cuh"
 #include "kda_internal.h"
+#include "kda_sm100.cuh"
 
 #include <cooperative_groups.h>
 
@@ -36,6 +37,9 @@ namespace cg = cooperative_groups;
 
 constexpr int kTokens = 4;  // of a thread
 constexpr int kMaxCluster = 16;  // above 8 a device may refuse a cluster size: B200 takes 16
+
+// Set where a wait gave up.
+__device__ unsigned g_recurrence_late;
 
 // Token range of sequence n: the dense batch's [n T, (n + 1) T), or the packed
 // offsets clamped into [0, T] (a decreasing pair is an empty sequence).
@@ -227,84 +231,211 @@ __device__ __forceinline__ void store_row(T* row, int c0, int col, int D, const 
     }
 }
 
-// Shared memory: the ring of stages, the spans of the token groups, the states that enter them, and the spans of the
-// parts of all CTAs of the cluster, by parity of the tile.
-template <typename T, int R, int THREADS> struct ScanSmem {
-    static constexpr int kGroups = THREADS / 8;             // token groups of a CTA (8 threads across the channels)
-    static constexpr int CT = 8 * Pack<T>::V;              // channels of a slice
+// Sizes, and shared memory: the ring of STAGES stages, the spans of the token groups, the states that enter them
+// (STATES copies), the spans of the CTA's parts, and the CTA's span by parity of the tile.
+template <typename T, int R, int THREADS, int STAGES, int STATES> struct ScanSmem {
+    static constexpr int V = Pack<T>::V, CT = 8 * V;        // channels of a thread, of a slice
+    static constexpr int kGroups = THREADS / 8;            // token groups of a CTA (8 threads across the channels)
+    static constexpr int kTile = kGroups * R;              // tokens
     static constexpr int kParts = THREADS / CT, kPer = kGroups / kParts;
     static constexpr int kSlot = R * THREADS * 16 + kGroups * R * 4;  // one tensor's tile, and a word more a token
-    static constexpr int kStage = 2 * kSlot, kStages = 2;
+    static constexpr int kStage = 2 * kSlot;
     static constexpr int kSpans = kGroups * CT * (int)sizeof(float2), kStates = kGroups * CT * (int)sizeof(float);
-    static constexpr int kBytes = kStages * kStage + kSpans + kStates + (kParts + 2) * CT * (int)sizeof(float2);
+    static constexpr int kBytes = STAGES * kStage + kSpans + STATES * kStates + kParts * CT * (int)sizeof(float2);
+
+    uint32_t* ring;
+    float4* spans;      // [group][pair of V/2][col]: A, H, A, H
+    float* states;      // [copy][group][quad of V/4][col][4]
+    float2* parts;      // [part][channel]
+    float2* whole;      // what follows
+    __device__ __forceinline__ explicit ScanSmem(unsigned char* smem) {
+        ring = reinterpret_cast<uint32_t*>(smem);
+        spans = reinterpret_cast<float4*>(smem + STAGES * kStage);
+        states = reinterpret_cast<float*>(smem + STAGES * kStage + kSpans);
+        parts = reinterpret_cast<float2*>(smem + STAGES * kStage + kSpans + STATES * kStates);
+        whole = parts + kParts * CT;
+    }
+    __device__ __forceinline__ uint32_t* stage(int k) const { return ring + k * (kStage / 4); }
 };
 
-// A cluster barrier that publishes this thread's writes to its own CTA's shared memory, and them alone: the full
-// release would wait for the tile's stores to global memory, 1.5 us.
-__device__ __forceinline__ void cluster_exchange() {
-    asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
-    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-    asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
-}
-
-// R: tokens of a thread. CLUSTER: the cluster has more than one CTA.
-template <typename T, int ALIGN, bool BWD, int R, int THREADS, bool CLUSTER>
-__global__ void __launch_bounds__(THREADS, 512 / THREADS) recurrence_scan_kernel(RecurrenceArgs a, int slices) {
-    using Sm = ScanSmem<T, R, THREADS>;
-    constexpr int V = Pack<T>::V, CT = Sm::CT, TILE = Sm::kGroups * R, PARTS = Sm::kParts, PER = Sm::kPer, S = Sm::kStages;
-    extern __shared__ __align__(16) unsigned char smem[];
-    uint32_t* ring = reinterpret_cast<uint32_t*>(smem);
-    float4* spans = reinterpret_cast<float4*>(smem + S * Sm::kStage);                  // [group][pair of V/2][col]: A, H, A, H
-    float* states = reinterpret_cast<float*>(smem + S * Sm::kStage + Sm::kSpans);      // [group][quad of V/4][col][4]
-    float2* parts = reinterpret_cast<float2*>(smem + S * Sm::kStage + Sm::kSpans + Sm::kStates);  // [part][channel]
-    float2* whole_of = parts + PARTS * CT;  // [parity][channel]: the CTA's span, read by the cluster
-    const int tid = threadIdx.x, col = tid & 7, group = tid >> 3;
-    int rank = 0, size = 1;
-    long long id = blockIdx.x;
-    if constexpr (CLUSTER) {
-        const cg::cluster_group cl = cg::this_cluster();
-        rank = (int)cl.block_rank();
-        size = (int)cl.num_blocks();
-        id /= size;
-    }
-    const int n = (int)(id / slices), c0 = (int)(id % slices) * CT, D = a.D;
+// What a thread knows of its sequence and slice, and the steps that both scan kernels take.
+template <typename T, int ALIGN, bool BWD, int R, int THREADS, typename Sm>
+struct Walk {
+    static constexpr int V = Sm::V, CT = Sm::CT, PER = Sm::kPer, PARTS = Sm::kParts;
+    const RecurrenceArgs& a;
+    int rank, size, n, c0, D, len, col, group;
     long long begin;
-    int len;
-    token_range(a.cu_seqlens, n, a.T, begin, len);
-    const T *la = (const T*)a.log_alpha + begin * D, *x = (const T*)a.x + begin * D;
-    const T* hf = BWD ? (const T*)a.h_fwd + begin * D : nullptr;
-    T* out = (T*)a.out + begin * D;
-    T* out_la = BWD ? (T*)a.out_la + begin * D : nullptr;
+    const T *la, *x, *hf, *la_stop, *x_stop;
+    T *out, *out_la;
+    // As (channel, part): channel p in the order of the spans, that is element e = 2 pair + half of thread column pcol.
+    int p, part, pair, pcol, half, pc;
 
-    // As (channel, part): channel p in the order of `spans`, that is element e = 2 pair + half of thread column pcol. Every
-    // part keeps the channel's state, by the same operations.
-    const int p = tid % CT, part = tid / CT, pair = p / 16, pcol = p % 16 / 2, half = p % 2;
-    const int pc = c0 + channel_of<T, ALIGN>(pcol, 2 * pair + half);
-    float state = pc < D && a.state0 ? a.state0[(long long)n * D + pc] : 0.f;
-    if constexpr (CLUSTER) cg::this_cluster().sync();  // every CTA has started, and has read its state
-
-    // token k of this CTA's tile `tile`, in walking order; -1: past the end
-    auto token = [&](int tile, int k) {
-        const unsigned at = (unsigned)(tile * size + rank) * TILE + k;  // below len + 16 TILE: no wrap
+    __device__ __forceinline__ Walk(const RecurrenceArgs& a_, long long id, int slices, int rank_, int size_) : a(a_), rank(rank_), size(size_) {
+        const int tid = threadIdx.x;
+        n = (int)(id / slices);
+        c0 = (int)(id % slices) * CT;
+        D = a.D;
+        token_range(a.cu_seqlens, n, a.T, begin, len);
+        la = (const T*)a.log_alpha + begin * D;
+        x = (const T*)a.x + begin * D;
+        hf = BWD ? (const T*)a.h_fwd + begin * D : nullptr;
+        out = (T*)a.out + begin * D;
+        out_la = BWD ? (T*)a.out_la + begin * D : nullptr;
+        const long long cells = (a.cu_seqlens ? 1ll : (long long)a.N) * a.T * D;  // the end of the tensors, for ALIGN 2
+        la_stop = (const T*)a.log_alpha + cells;
+        x_stop = (const T*)a.x + cells;
+        col = tid & 7;
+        group = tid >> 3;
+        p = tid % CT;
+        part = tid / CT;
+        pair = p / 16;
+        pcol = p % 16 / 2;
+        half = p % 2;
+        pc = c0 + channel_of<T, ALIGN>(pcol, 2 * pair + half);
+    }
+    __device__ __forceinline__ int tiles() const {
+        const long long step = (long long)size * Sm::kTile;
+        return (int)((len + step - 1) / step);
+    }
+    __device__ __forceinline__ float first_state() const { return pc < D && a.state0 ? a.state0[(long long)n * D + pc] : 0.f; }
+    __device__ __forceinline__ void last_state(float s) const {
+        if (part == 0 && rank == 0 && pc < D && a.state_end) a.state_end[(long long)n * D + pc] = s;
+    }
+    // number, in walking order, of token k of this CTA's tile `tile`: below len + 16 tiles, so no wrap
+    __device__ __forceinline__ unsigned number(int tile, int k) const { return (unsigned)(tile * size + rank) * Sm::kTile + k; }
+    // the token itself; -1: past the end
+    __device__ __forceinline__ int token(int tile, int i) const {
+        const unsigned at = number(tile, group * R + i);
         return at < (unsigned)len ? (BWD ? len - 1 - (int)at : (int)at) : -1;
-    };
-    constexpr int kSlot = Sm::kSlot / 4;
-    // the end of the tensors, for ALIGN 2
-    const long long cells = (a.cu_seqlens ? 1ll : (long long)a.N) * a.T * D;
-    const T *la_stop = (const T*)a.log_alpha + cells, *x_stop = (const T*)a.x + cells;
-    auto fetch = [&](int tile) {
-        uint32_t* to = ring + (tile & 1) * 2 * kSlot;
-        const long long at = (long long)(tile * size + rank) * TILE;
-        const int left = (int)min(max(len - at, 0ll), (long long)TILE);
+    }
+    __device__ __forceinline__ void fetch(uint32_t* to, int tile) const {
+        const long long at = number(tile, 0);
+        const int left = (int)min(max(len - at, 0ll), (long long)Sm::kTile);
         const long long row = (BWD ? len - 1 - at : at) * D;
         copy_tile<T, ALIGN, R, THREADS>(to, la + row, BWD ? -D : D, left, c0, D, la_stop);
-        copy_tile<T, ALIGN, R, THREADS>(to + kSlot, x + row, BWD ? -D : D, left, c0, D, x_stop);
-    };
-    const long long step = (long long)size * TILE;
-    const int tiles = (int)((len + step - 1) / step);
+        copy_tile<T, ALIGN, R, THREADS>(to + Sm::kSlot / 4, x + row, BWD ? -D : D, left, c0, D, x_stop);
+    }
+    // Token i of a fetched tile.
+    __device__ __forceinline__ void read(const uint32_t* from, int tile, int i, Pack<T>& pl, Pack<T>& px) const {
+        // D is odd and the tensors begin on 16 bytes: every other row begins in the middle of a word
+        // (those past the end, which hold zeros, counted on: the copy goes by the same rows)
+        const unsigned at = number(tile, group * R + i);
+        const bool odd = ALIGN == 2 && (((unsigned)begin + (BWD ? len - 1 - at : at)) & 1);
+        pl = slot_of<T, ALIGN, R, THREADS>(from, i, odd);
+        px = slot_of<T, ALIGN, R, THREADS>(from + Sm::kSlot / 4, i, odd);
+    }
+    // h_{t-1} of the thread's tokens (zeros for the first token, whose is h0)
+    __device__ __forceinline__ void read_before(int tile, Pack<T> (&ph)[R]) const {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int t = token(tile, i);
+            ph[i] = read_row<T, ALIGN>(hf + (long long)max(t - 1, 0) * D, c0, col, D, t > 0);
+        }
+    }
+    __device__ __forceinline__ static void decays(const Pack<T>& pl, F2 (&d)[V / 2]) {
+#pragma unroll
+        for (int e = 0; e < V / 2; ++e) d[e] = f2(decay<T>(pl.get(2 * e)), decay<T>(pl.get(2 * e + 1)));
+    }
+    // (A, H) <- the token after (A, H)
+    __device__ __forceinline__ static void compose(bool first, const F2 (&d)[V / 2], const Pack<T>& px, F2 (&A)[V / 2], F2 (&H)[V / 2]) {
+#pragma unroll
+        for (int e = 0; e < V / 2; ++e) {
+            const F2 v = f2(px.get(2 * e), px.get(2 * e + 1));
+            A[e] = first ? d[e] : f2_mul(A[e], d[e]);
+            if (BWD) H[e] = f2_mul(d[e], first ? v : f2_add(H[e], v));
+            else H[e] = first ? v : f2_fma(d[e], H[e], v);
+        }
+    }
+    __device__ __forceinline__ void put_span(const Sm& sm, const F2 (&A)[V / 2], const F2 (&H)[V / 2]) const {
+#pragma unroll
+        for (int e = 0; e < V / 2; ++e) {
+            const float2 A_ = f2_parts(A[e]), H_ = f2_parts(H[e]);
+            sm.spans[(group * (V / 2) + e) * 8 + col] = make_float4(A_.x, H_.x, A_.y, H_.y);
+        }
+    }
+    // The spans of this part's groups; the part's span goes to sm.parts.
+    __device__ __forceinline__ void part_span(const Sm& sm, float2 (&w)[PER]) const {
+#pragma unroll
+        for (int k = 0; k < PER; ++k)
+            w[k] = reinterpret_cast<const float2*>(sm.spans)[((part * PER + k) * (V / 2) + pair) * 16 + pcol * 2 + half];
+        float2 all = w[0];
+#pragma unroll
+        for (int k = 1; k < PER; ++k) all = make_float2(all.x * w[k].x, fmaf(w[k].x, all.y, w[k].y));
+        sm.parts[part * CT + p] = all;
+    }
+    // Of the CTA's parts: those before this one, all.
+    __device__ __forceinline__ void whole_span(const Sm& sm, float2& before, float2& whole) const {
+        before = whole = make_float2(1.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < PARTS; ++k) {
+            const float2 u = sm.parts[k * CT + p];
+            if (k == part) before = whole;
+            whole = make_float2(whole.x * u.x, fmaf(u.x, whole.y, u.y));
+        }
+    }
+    // The states that enter this part's groups, from the one that enters the part.
+    __device__ __forceinline__ void put_states(float* states, float s, const float2 (&w)[PER]) const {
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            states[(((part * PER + k) * (V / 4) + pair / 2) * 8 + pcol) * 4 + (pair & 1) * 2 + half] = s;
+            s = fmaf(w[k].x, s, w[k].y);
+        }
+    }
+    __device__ __forceinline__ void own_state(const float* states, F2 (&cur)[V / 2]) const {
+#pragma unroll
+        for (int q = 0; q < V / 4; ++q) {
+            const float4 v = reinterpret_cast<const float4*>(states)[(group * (V / 4) + q) * 8 + col];
+            cur[2 * q] = f2(v.x, v.y);
+            cur[2 * q + 1] = f2(v.z, v.w);
+        }
+    }
+    // Token i from the state that enters it: writes its outputs, moves the state on.
+    __device__ __forceinline__ void run_token(int tile, int i, const F2 (&d)[V / 2], const Pack<T>& px, const Pack<T>& ph, F2 (&cur)[V / 2]) const {
+        const int t = token(tile, i);
+        float y[V], z[V];
+#pragma unroll
+        for (int e = 0; e < V / 2; ++e) {
+            const F2 v = f2(px.get(2 * e), px.get(2 * e + 1));
+            F2 o;
+            if constexpr (BWD) {
+                o = f2_add(cur[e], v);
+                cur[e] = f2_mul(d[e], o);
+                float b0 = ph.get(2 * e), b1 = ph.get(2 * e + 1);
+                if (t == 0) {
+                    const int e0 = c0 + channel_of<T, ALIGN>(col, 2 * e), e1 = c0 + channel_of<T, ALIGN>(col, 2 * e + 1);
+                    b0 = a.h0 && e0 < D ? a.h0[(long long)n * D + e0] : 0.f;
+                    b1 = a.h0 && e1 < D ? a.h0[(long long)n * D + e1] : 0.f;
+                }
+                const float2 zz = f2_parts(f2_mul(cur[e], f2(b0, b1)));
+                z[2 * e] = zz.x;
+                z[2 * e + 1] = zz.y;
+            } else {
+                o = cur[e] = f2_fma(d[e], cur[e], v);
+            }
+            const float2 yy = f2_parts(o);
+            y[2 * e] = yy.x;
+            y[2 * e + 1] = yy.y;
+        }
+        if (t >= 0) {
+            store_row<T, ALIGN>(out + (long long)t * D, c0, col, D, y);
+            if constexpr (BWD) store_row<T, ALIGN>(out_la + (long long)t * D, c0, col, D, z);
+        }
+    }
+};
+
+// One CTA a row. R: tokens of a thread.
+template <typename T, int ALIGN, bool BWD, int R, int THREADS>
+__global__ void __launch_bounds__(THREADS, 512 / THREADS) recurrence_scan_kernel(RecurrenceArgs a, int slices) {
+    constexpr int S = 2;
+    using Sm = ScanSmem<T, R, THREADS, S, 1>;
+    constexpr int V = Sm::V;
+    extern __shared__ __align__(16) unsigned char smem[];
+    const Sm sm(smem);
+    const Walk<T, ALIGN, BWD, R, THREADS, Sm> walk(a, blockIdx.x, slices, 0, 1);
+    float state = walk.first_state();  // every part keeps its channel's, by the same operations
+    const int tiles = walk.tiles();
     for (int k = 0; k < S; ++k) {
-        if (k < tiles) fetch(k);
+        if (k < tiles) walk.fetch(sm.stage(k), k);
         cp_async_commit();
     }
     for (int tile = 0; tile < tiles; ++tile) {
@@ -312,136 +443,163 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) recurrence_scan_kernel
         cp_async_wait<S - 1>();
         if constexpr (ALIGN != 16) __syncwarp();
         F2 d[R][V / 2], A[V / 2], H[V / 2];
-        Pack<T> px[R], ph[BWD ? R : 1];
-        if constexpr (BWD) {  // h_{t-1}: read now, used at the tile's end
+        Pack<T> px[R], ph[R];
+        if constexpr (BWD) walk.read_before(tile, ph);  // used at the tile's end
 #pragma unroll
-            for (int i = 0; i < R; ++i) {
-                const int t = token(tile, group * R + i);
-                ph[i] = read_row<T, ALIGN>(hf + (long long)max(t - 1, 0) * D, c0, col, D, t > 0);
-            }
-        }
-        {
-            const uint32_t* from = ring + (tile & 1) * 2 * kSlot;
-#pragma unroll
-            for (int i = 0; i < R; ++i) {
-                // D is odd and the tensors begin on 16 bytes: every other row begins in the middle of a word
-                // (those past the end, which hold zeros, counted on: the copy goes by the same rows)
-                const unsigned at = (unsigned)(tile * size + rank) * TILE + group * R + i;
-                const bool odd = ALIGN == 2 && (((unsigned)begin + (BWD ? len - 1 - at : at)) & 1);
-                const Pack<T> pl = slot_of<T, ALIGN, R, THREADS>(from, i, odd);
-                px[i] = slot_of<T, ALIGN, R, THREADS>(from + kSlot, i, odd);
-#pragma unroll
-                for (int e = 0; e < V / 2; ++e) {
-                    d[i][e] = f2(decay<T>(pl.get(2 * e)), decay<T>(pl.get(2 * e + 1)));
-                    const F2 v = f2(px[i].get(2 * e), px[i].get(2 * e + 1));
-                    if (i == 0) {
-                        A[e] = d[i][e];
-                        H[e] = BWD ? f2_mul(d[i][e], v) : v;
-                    } else {
-                        A[e] = f2_mul(A[e], d[i][e]);
-                        H[e] = BWD ? f2_mul(d[i][e], f2_add(H[e], v)) : f2_fma(d[i][e], H[e], v);
-                    }
-                }
-            }
+        for (int i = 0; i < R; ++i) {
+            Pack<T> pl;
+            walk.read(sm.stage(tile & 1), tile, i, pl, px[i]);
+            walk.decays(pl, d[i]);
+            walk.compose(i == 0, d[i], px[i], A, H);
         }
         if constexpr (ALIGN != 16) __syncwarp();
-        if (tile + S < tiles) fetch(tile + S);
+        if (tile + S < tiles) walk.fetch(sm.stage(tile & 1), tile + S);
         cp_async_commit();
-#pragma unroll
-        for (int e = 0; e < V / 2; ++e) {
-            const float2 A_ = f2_parts(A[e]), H_ = f2_parts(H[e]);
-            spans[(group * (V / 2) + e) * 8 + col] = make_float4(A_.x, H_.x, A_.y, H_.y);
-        }
+        walk.put_span(sm, A, H);
         __syncthreads();
         // 2. as (channel, part): the part's span, the CTA's
-        float2 w[PER];
-#pragma unroll
-        for (int k = 0; k < PER; ++k)
-            w[k] = reinterpret_cast<const float2*>(spans)[((part * PER + k) * (V / 2) + pair) * 16 + pcol * 2 + half];
-        float2 all = w[0];
-#pragma unroll
-        for (int k = 1; k < PER; ++k) all = make_float2(all.x * w[k].x, fmaf(w[k].x, all.y, w[k].y));
-        parts[part * CT + p] = all;
+        float2 w[Sm::kPer], before, whole;
+        walk.part_span(sm, w);
         __syncthreads();
-        float2 before = make_float2(1.f, 0.f), whole = before;  // of the CTA's parts: those before this one, all
-#pragma unroll
-        for (int k = 0; k < PARTS; ++k) {
-            const float2 u = parts[k * CT + p];
-            if (k == part) before = whole;
-            whole = make_float2(whole.x * u.x, fmaf(u.x, whole.y, u.y));
-        }
-        // 3. the state that enters this part's groups; the state after the cluster's tile
-        float s = state;
-        if constexpr (CLUSTER) {
-            float2* mine = whole_of + (tile & 1) * CT + p;
-            if (part == 0) *mine = whole;
-            cluster_exchange();
-            for (int r0 = 0; r0 < size; r0 += 8) {
-                float2 u[8];
-#pragma unroll
-                for (int r = 0; r < 8; ++r)
-                    if (r0 + r < size) u[r] = *cg::this_cluster().map_shared_rank(mine, r0 + r);
-#pragma unroll
-                for (int r = 0; r < 8; ++r)
-                    if (r0 + r < size) {
-                        if (r0 + r == rank) s = state;
-                        state = fmaf(u[r].x, state, u[r].y);
-                    }
-            }
-        } else {
-            state = fmaf(whole.x, state, whole.y);
-        }
-        s = fmaf(before.x, s, before.y);
-#pragma unroll
-        for (int k = 0; k < PER; ++k) {
-            states[(((part * PER + k) * (V / 4) + pair / 2) * 8 + pcol) * 4 + (pair & 1) * 2 + half] = s;
-            s = fmaf(w[k].x, s, w[k].y);
-        }
+        walk.whole_span(sm, before, whole);
+        // 3. the state that enters this part's groups; the state after the tile
+        walk.put_states(sm.states, fmaf(before.x, state, before.y), w);
+        state = fmaf(whole.x, state, whole.y);
         __syncthreads();
         // 4. the tokens again, from the state that enters them
         F2 cur[V / 2];
+        walk.own_state(sm.states, cur);
 #pragma unroll
-        for (int q = 0; q < V / 4; ++q) {
-            const float4 v = reinterpret_cast<const float4*>(states)[(group * (V / 4) + q) * 8 + col];
-            cur[2 * q] = f2(v.x, v.y);
-            cur[2 * q + 1] = f2(v.z, v.w);
-        }
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const int t = token(tile, group * R + i);
-            float y[V], z[V];
-#pragma unroll
-            for (int e = 0; e < V / 2; ++e) {
-                const F2 v = f2(px[i].get(2 * e), px[i].get(2 * e + 1));
-                F2 o;
-                if constexpr (BWD) {
-                    o = f2_add(cur[e], v);
-                    cur[e] = f2_mul(d[i][e], o);
-                    float b0 = ph[i].get(2 * e), b1 = ph[i].get(2 * e + 1);
-                    if (t == 0) {
-                        const int e0 = c0 + channel_of<T, ALIGN>(col, 2 * e), e1 = c0 + channel_of<T, ALIGN>(col, 2 * e + 1);
-                        b0 = a.h0 && e0 < D ? a.h0[(long long)n * D + e0] : 0.f;
-                        b1 = a.h0 && e1 < D ? a.h0[(long long)n * D + e1] : 0.f;
-                    }
-                    const float2 zz = f2_parts(f2_mul(cur[e], f2(b0, b1)));
-                    z[2 * e] = zz.x;
-                    z[2 * e + 1] = zz.y;
-                } else {
-                    o = cur[e] = f2_fma(d[i][e], cur[e], v);
-                }
-                const float2 yy = f2_parts(o);
-                y[2 * e] = yy.x;
-                y[2 * e + 1] = yy.y;
-            }
-            if (t >= 0) {
-                store_row<T, ALIGN>(out + (long long)t * D, c0, col, D, y);
-                if constexpr (BWD) store_row<T, ALIGN>(out_la + (long long)t * D, c0, col, D, z);
-            }
-        }
+        for (int i = 0; i < R; ++i) walk.run_token(tile, i, d[i], px[i], ph[i], cur);
     }
     cp_async_wait<0>();
-    if constexpr (CLUSTER) cg::this_cluster().sync();  // no CTA ends while another reads its shared memory
-    if (part == 0 && rank == 0 && pc < D && a.state_end) a.state_end[(long long)n * D + pc] = state;
+    walk.last_state(state);
+}
+
+// A 64-bit store into the shared memory of CTA `rank` of the cluster, counted there by the mbarrier at the same place as
+// `bar` here. It needs no fence: a cluster barrier with its release would wait for the stores to global memory, 1 us.
+__device__ __forceinline__ void push(const void* to, uint64_t* bar, int rank, float2 x) {
+    uint32_t at, b;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(sm100::smem_u32(to)), "r"(rank));
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(sm100::smem_u32(bar)), "r"(rank));
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(at),
+                 "r"(__float_as_uint(x.x)), "r"(__float_as_uint(x.y)), "r"(b)
+                 : "memory");
+}
+
+// A cluster of CTAs a row, where rows are few: what counts is the time of one round of tiles. So the rounds overlap: the
+// spans of tile k + 1 are composed and handed to the cluster before tile k is run, and the exchange of tile k has tile
+// k - 1's run to finish in. The spans are pushed into every CTA's inbox and counted by its mbarrier; a wait that is not
+// met in a.wait_cycles sets g_recurrence_late, and the kernel ends without waiting, pushing or arming a barrier again (the
+// others' next waits then give up too). An inbox slot is written again two tiles later, when its owner has sent the tile
+// between, which it does after having read the slot and armed its barrier again.
+template <typename T, int ALIGN, bool BWD, int R, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1) recurrence_cluster_kernel(RecurrenceArgs a, int slices) {
+    constexpr int S = 4;
+    using Sm = ScanSmem<T, R, THREADS, S, 2>;
+    constexpr int V = Sm::V, CT = Sm::CT;
+    extern __shared__ __align__(16) unsigned char smem[];
+    const Sm sm(smem);
+    const cg::cluster_group cluster = cg::this_cluster();
+    const int rank = (int)cluster.block_rank(), size = (int)cluster.num_blocks();
+    const Walk<T, ALIGN, BWD, R, THREADS, Sm> walk(a, blockIdx.x / size, slices, rank, size);
+    float state = walk.first_state();
+    float2* inbox = sm.whole;  // [parity][rank][channel]: the CTAs' spans
+    uint64_t* bar = reinterpret_cast<uint64_t*>(inbox + 2 * kMaxCluster * CT);  // [parity]: they have arrived
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) sm100::mbar_init(bar + i, 1);
+        sm100::fence_mbar_init();
+        for (int i = 0; i < 2; ++i) sm100::mbar_arrive_expect_tx(bar + i, size * CT * 8);
+    }
+    cluster.sync();  // every CTA has started, has read its state and set up its barriers
+    const int tiles = walk.tiles();
+#pragma unroll 1
+    for (int k = 0; k < S - 1; ++k) {
+        if (k < tiles) walk.fetch(sm.stage(k), k);
+        cp_async_commit();
+    }
+    float2 w[Sm::kPer], before = make_float2(1.f, 0.f);
+    bool late = false;  // a wait gave up
+    // decays and inputs of the tile that is run, and of the one after it
+    F2 d[R][V / 2], d1[R][V / 2];
+    Pack<T> px[R], px1[R];
+    // the thread's span of a tile that has arrived
+    auto span = [&](int tile, F2 (&A)[V / 2], F2 (&H)[V / 2]) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            Pack<T> pl;
+            walk.read(sm.stage(tile % S), tile, i, pl, px1[i]);
+            walk.decays(pl, d1[i]);
+            walk.compose(i == 0, d1[i], px1[i], A, H);
+        }
+    };
+    // from the spans in shared memory to the CTA's span, handed to the cluster
+    auto publish = [&](int tile) {
+        walk.part_span(sm, w);
+        __syncthreads();
+        float2 whole;
+        walk.whole_span(sm, before, whole);
+        if (late || (a.test_withhold && rank == 0)) return;
+        for (int r = walk.part; r < size; r += Sm::kParts) push(inbox + ((tile & 1) * kMaxCluster + rank) * CT + walk.p, bar + (tile & 1), r, whole);
+    };
+    if (tiles > 0) {
+        cp_async_wait<S - 2>();
+        if constexpr (ALIGN != 16) __syncwarp();
+        F2 A[V / 2], H[V / 2];
+        span(0, A, H);
+        walk.put_span(sm, A, H);
+        __syncthreads();
+        publish(0);
+    }
+#pragma unroll 1
+    for (int tile = 0; tile < tiles; ++tile) {
+        const bool more = tile + 1 < tiles;
+        if constexpr (ALIGN != 16) __syncwarp();  // the stage that is filled next was read by the whole warp
+        if (tile + S - 1 < tiles) walk.fetch(sm.stage((tile + S - 1) % S), tile + S - 1);
+        cp_async_commit();
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            px[i] = px1[i];
+#pragma unroll
+            for (int e = 0; e < V / 2; ++e) d[i][e] = d1[i][e];
+        }
+        Pack<T> ph[R];
+        if constexpr (BWD) walk.read_before(tile, ph);
+        F2 A[V / 2], H[V / 2];
+        if (more) {
+            cp_async_wait<S - 2>();
+            if constexpr (ALIGN != 16) __syncwarp();
+            span(tile + 1, A, H);
+        }
+        // the state that enters this CTA's tile; the state after the cluster's
+        if (!late) late = !sm100::mbar_wait_bounded(bar + (tile & 1), (tile >> 1) & 1, a.wait_cycles);
+        const float2* theirs = inbox + (tile & 1) * kMaxCluster * CT + walk.p;
+        float s = state;
+        for (int r = 0; r < size; ++r) {
+            const float2 u = theirs[r * CT];
+            if (r == rank) s = state;
+            state = fmaf(u.x, state, u.y);
+        }
+        // of tile + 2. Only after a phase that was completed: a barrier must get no arrival more than a phase takes.
+        if (threadIdx.x == 0 && !late) sm100::mbar_arrive_expect_tx(bar + (tile & 1), size * CT * 8);
+        float* states = sm.states + (tile & 1) * (Sm::kStates / 4);
+        walk.put_states(states, fmaf(before.x, s, before.y), w);
+        if (more) walk.put_span(sm, A, H);
+        __syncthreads();
+        if (more) publish(tile + 1);
+        F2 cur[V / 2];
+        walk.own_state(states, cur);
+#pragma unroll
+        for (int i = 0; i < R; ++i) walk.run_token(tile, i, d[i], px[i], ph[i], cur);
+    }
+    cp_async_wait<0>();
+    if (late) {
+        g_recurrence_late = 1;
+        // what others have pushed lands in microseconds: not in the shared memory of a CTA that has ended
+        for (const long long t0 = clock64(); clock64() - t0 < (1ll << 17);) {}
+    }
+    cluster.sync();  // no CTA ends while another may still write to its shared memory
+    walk.last_state(state);
 }
 
 // One token: four cells a thread, 16 bytes of state (the tensors are contiguous, so their rows do not matter).
@@ -483,25 +641,38 @@ __global__ void __launch_bounds__(256) recurrence_step_kernel(const T* log_alpha
     }
 }
 
-template <typename T, int ALIGN, bool BWD, int THREADS, bool CLUSTER>
-cudaError_t launch_scan_as(const RecurrenceArgs& a, int slices, int size, cudaStream_t stream) {
-    using Sm = ScanSmem<T, kTokens, THREADS>;
-    auto kernel = recurrence_scan_kernel<T, ALIGN, BWD, kTokens, THREADS, CLUSTER>;
+template <typename T, int ALIGN, bool BWD, int THREADS>
+cudaError_t launch_rows(const RecurrenceArgs& a, int slices, cudaStream_t stream) {
+    using Sm = ScanSmem<T, kTokens, THREADS, 2, 1>;
+    auto kernel = recurrence_scan_kernel<T, ALIGN, BWD, kTokens, THREADS>;
+    static std::atomic<unsigned long long> raised{0};
+    const cudaError_t err = allow_smem(kernel, Sm::kBytes, raised);
+    if (err != cudaSuccess) return err;
+    kernel<<<(unsigned)((long long)a.N * slices), THREADS, Sm::kBytes, stream>>>(a, slices);
+    return cudaGetLastError();
+}
+
+template <typename T, int ALIGN, bool BWD>
+cudaError_t launch_clusters(const RecurrenceArgs& a, int slices, int size, cudaStream_t stream) {
+    constexpr int THREADS = 256;
+    using Sm = ScanSmem<T, kTokens, THREADS, 4, 2>;
+    constexpr int kBytes = Sm::kBytes + 2 * kMaxCluster * Sm::CT * (int)sizeof(float2) + 16;
+    auto kernel = recurrence_cluster_kernel<T, ALIGN, BWD, kTokens, THREADS>;
     static std::atomic<unsigned long long> raised{0};
     cudaError_t err = size > 8 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) : cudaSuccess;
-    if (err == cudaSuccess) err = allow_smem(kernel, Sm::kBytes, raised);
+    if (err == cudaSuccess) err = allow_smem(kernel, kBytes, raised);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((long long)a.N * slices * size));
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = Sm::kBytes;
+    cfg.dynamicSmemBytes = kBytes;
     cfg.stream = stream;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = size;
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
-    cfg.numAttrs = CLUSTER ? 1 : 0;
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, a, slices);
 }
 
@@ -511,21 +682,22 @@ cudaError_t launch_scan(const RecurrenceArgs& a, cudaStream_t stream) {
     const int slices = (a.D + CT - 1) / CT;
     const long long rows = (long long)a.N * slices;
     const long long tokens = a.cu_seqlens ? (a.T + a.N - 1) / a.N : a.T;
-    // CTAs of a cluster: one from 75 rows on (128 rows, T 8192 backward: 127 us, with two 131; 96 rows, T 4096: 36 and
-    // 44); below, as many as fill two CTAs on each SM, so that one computes while the other exchanges (64 rows, T 4096:
-    // 24 us with four, 31 with two, 40 with one), no more than the tokens give tiles to; sixteen only where all clusters
-    // of them fit at once (T 16384: six rows 27 us, with eight 34; eight rows 37 and 34).
+    // CTAs of a cluster. From 75 rows on one: the rows alone fill the SMs (128 rows, T 8192 backward: 127 us, with two
+    // 131). Below, as many as fit on the GPU at once, one an SM, where a cluster takes SMs of one GPC: six clusters of
+    // sixteen (four rows, T 65536: 52 us, with eight 98), fourteen of eight (twelve rows, T 32768: 53 us, with sixteen 57),
+    // thirty-four of four (32 rows, T 16384: 52 us, with two 89), else two; 15 and 16 rows take clusters of sixteen in two
+    // rounds (T 32768: 82 us, with four 97). No more than the tokens give tiles to.
+    const int most = rows <= 6 ? 16 : rows <= 14 ? 8 : rows <= 16 ? 16 : rows <= 34 ? 4 : rows < 75 ? 2 : 1;
     int size = 1;
-    while (rows < 75 && size < (rows <= 6 ? kMaxCluster : 8) && rows * size * 2 <= 2 * 148 &&
-           (long long)size * (256 / 8) * kTokens < tokens)
-        size *= 2;
-    if (size > 1) return launch_scan_as<T, ALIGN, BWD, 256, true>(a, slices, size, stream);
+    while (size < most && (long long)size * (256 / 8) * kTokens < tokens) size *= 2;
+    if (a.test_withhold && size == 1) return cudaErrorInvalidValue;
+    if (size > 1) return launch_clusters<T, ALIGN, BWD>(a, slices, size, stream);
     // One CTA of 512 threads on an SM takes tiles of twice the tokens, and its SM's share of the bandwidth with fewer
     // barriers: 256 rows, T 8192 132 us (two CTAs of 256 threads: 150); 96 rows, T 4096 backward 51 (65). It pays where
     // the rows fill their rounds of 148 (192 rows: 67 us against 57) and there are tokens enough (T 200: 7.4 against 5.8).
     const long long rounds = (rows + 147) / 148;
-    if (tokens >= 512 && (rounds == 1 || rows * 5 >= rounds * 148 * 4)) return launch_scan_as<T, ALIGN, BWD, 512, false>(a, slices, 1, stream);
-    return launch_scan_as<T, ALIGN, BWD, 256, false>(a, slices, 1, stream);
+    if (tokens >= 512 && (rounds == 1 || rows * 5 >= rounds * 148 * 4)) return launch_rows<T, ALIGN, BWD, 512>(a, slices, stream);
+    return launch_rows<T, ALIGN, BWD, 256>(a, slices, stream);
 }
 
 template <bool BWD> cudaError_t launch_scan_any(const RecurrenceArgs& a, cudaStream_t stream) {
@@ -541,6 +713,13 @@ template <bool BWD> cudaError_t launch_scan_any(const RecurrenceArgs& a, cudaStr
 
 cudaError_t launch_recurrence_fwd(const RecurrenceArgs& a, cudaStream_t stream) { return launch_scan_any<false>(a, stream); }
 cudaError_t launch_recurrence_bwd(const RecurrenceArgs& a, cudaStream_t stream) { return launch_scan_any<true>(a, stream); }
+
+cudaError_t recurrence_late(unsigned* flag) {
+    cudaError_t err = cudaMemcpyFromSymbol(flag, g_recurrence_late, sizeof(*flag));
+    const unsigned zero = 0;
+    if (err == cudaSuccess && *flag) err = cudaMemcpyToSymbol(g_recurrence_late, &zero, sizeof(zero));
+    return err;
+}
 
 cudaError_t launch_recurrence_step(const void* la, const void* x, const float* h_in, float* h_out, void* y,
                                    long long cells, int bf16, cudaStream_t stream) {

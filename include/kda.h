@@ -49,7 +49,8 @@ typedef enum {
     KDA_ERR_INVALID_ARG = 1, /* null pointer, bad size, misaligned pointer, workspace too small */
     KDA_ERR_UNSUPPORTED = 2, /* valid but not implemented (head size, chunk size, dtype) */
     KDA_ERR_CUDA = 3,        /* a CUDA launch or query failed; see cudaGetLastError */
-    KDA_ERR_TIMEOUT = 4      /* a bounded device-side wait expired (kda_workspace_status, kda_noalloc_status) */
+    KDA_ERR_TIMEOUT = 4      /* a bounded device-side wait expired (kda_workspace_status, kda_noalloc_status,
+                                kda_recurrence_status) */
 } kda_status_t;
 
 typedef enum { KDA_F32 = 0, KDA_BF16 = 1 } kda_dtype_t;
@@ -381,6 +382,25 @@ kda_status_t kda_recurrence_fwd(const void *log_alpha, const void *x, const floa
 kda_status_t kda_recurrence_bwd(const void *log_alpha, const void *h, const float *h0, const void *d_h,
                                 const float *d_h_T, void *d_x, void *d_log_alpha, float *d_h0,
                                 const int *cu_seqlens, int N, int T, int D, kda_dtype_t dtype, void *stream);
+
+/*
+ * Where sequences times channels are few, the scan of kda_recurrence_fwd and
+ * _bwd runs on clusters of CTAs that hand one another the state; each of their
+ * waits gives up after about one second of SM clock, sets a flag in the library
+ * and lets the kernel end (its outputs are then invalid). kda_recurrence_status
+ * synchronises `stream` and returns KDA_ERR_TIMEOUT if that has happened on the
+ * current device since it was last asked, and clears the flag; else KDA_OK, or
+ * KDA_ERR_CUDA if the stream reported an error. No other call of this section
+ * waits on anything.
+ * kda_recurrence_timeout_test is a test hook for that path (not for production
+ * use): the dense forward pass without states, with the first CTA of every
+ * cluster sending nothing and a wait budget in [1, 2^31] cycles. h is undefined
+ * after it; later calls are unaffected. Needs few rows (N * ceil(D / 32) < 75)
+ * and T >= 512 (else KDA_ERR_INVALID_ARG).
+ */
+kda_status_t kda_recurrence_status(void *stream);
+kda_status_t kda_recurrence_timeout_test(const void *log_alpha, const void *x, void *h, int N, int T, int D,
+                                         kda_dtype_t dtype, long long wait_budget_cycles, void *stream);
 
 /* One token per sequence: h_out = exp(log_alpha) * h_in + x, y = h_out rounded
  * to dtype. log_alpha, x, y [N, D] dtype; h_in, h_out [N, D] float (h_out may

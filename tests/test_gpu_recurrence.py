@@ -242,6 +242,17 @@ def test_equal_bits_and_streams_and_graphs(cuda_lib):
             assert torch.equal(g2[name], grads[name]), name
 
 
+@pytest.mark.parametrize("rows", [1, 6, 7, 14, 15, 16, 17, 34, 35, 74, 75, 148, 149])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_every_cluster_size(cuda_lib, dtype, rows):
+    """The numbers of rows (slices of 128 bytes of channels) at which another split is taken."""
+    D = rows * (64 if dtype == "bf16" else 32)
+    log_alpha, x, g = draw((1, 2600, D), DT[dtype], 90 + rows)
+    h0 = torch.randn(1, D, generator=g)
+    h, _ = check_fwd(cuda_lib, log_alpha, x, h0)
+    check_bwd(cuda_lib, log_alpha, h.cpu(), h0, x, h0)
+
+
 def test_offsets_past_32_bits(cuda_lib):
     """More than 2^31 elements: the last tokens of the last channels, whose memory is a few tokens."""
     T, D, tail = 530000, 4104, 100

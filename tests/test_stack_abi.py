@@ -35,6 +35,15 @@ def test_recurrence_bwd_refuses(bad):
     assert rec_bwd(**bad) == 1
 
 
+def test_recurrence_timeout_hook_refuses():
+    f = kda.load().kda_recurrence_timeout_test
+    good = dict(la=P[0], x=P[1], h=P[2], N=1, T=600, D=64, dtype=1, budget=1 << 20)
+    for bad in (dict(budget=0), dict(budget=-1), dict(budget=(1 << 31) + 1), dict(T=100), dict(D=4096), dict(N=0), dict(N=40, D=128),
+                dict(x=None), dict(h=ODD), dict(dtype=5)):
+        a = {**good, **bad}
+        assert f(a["la"], a["x"], a["h"], a["N"], a["T"], a["D"], a["dtype"], a["budget"], None) == 1, bad
+
+
 def test_recurrence_step_refuses():
     f = kda.load().kda_recurrence_step
     good = P[:5]
