@@ -172,7 +172,8 @@ def _on(device):
 
 
 def _need(t, name, shape, dtype, device):
-    if t.dtype == dtype and t.shape == shape and t.is_contiguous() and t.device == device and t.is_cuda:
+    # get_device() is the index of a CUDA tensor's device, -1 for others; device.index is None for the CPU
+    if t.dtype == dtype and t.shape == shape and t.is_contiguous() and t.get_device() == device.index:
         return
     if not t.is_cuda:
         raise ValueError(f"{name}: must be a CUDA tensor (this library has no CPU path)")
@@ -748,7 +749,7 @@ def attn_decode(q, k_cache, v_cache, page_table, seq_lens, *, k=None, v=None, sc
         _need(k, "k", (N, Hk, d), dt, dev)
         _need(v, "v", (N, Hk, d), dt, dev)
     if o is None:
-        o = torch.empty(N, Hq, d, dtype=dt, device=dev)
+        o = torch.empty_like(q)
     else:
         _need(o, "o", (N, Hq, d), dt, dev)
     if lse is not None:

@@ -69,7 +69,7 @@ def test_forward_and_backward(cuda_lib, dtype, shape):
     check_bwd(cuda_lib, log_alpha, h.cpu(), None, dh, None)
 
 
-@pytest.mark.parametrize("lens", [[5], [0], [0, 1, 130, 0, 17], [128, 128, 1, 257], [1] * 40, [900, 3, 0]])
+@pytest.mark.parametrize("lens", [[5], [0], [0, 1, 130, 0, 17], [128, 128, 1, 257], [1] * 40, [900, 3, 0], [0, 3000, 1, 700]])
 @pytest.mark.parametrize("D", [8, 50, 192])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_packed(cuda_lib, dtype, D, lens):
@@ -240,6 +240,23 @@ def test_equal_bits_and_streams_and_graphs(cuda_lib):
         assert torch.equal(got, want[0]) and torch.equal(got_end, want[1])
         for name in grads:
             assert torch.equal(g2[name], grads[name]), name
+
+
+def test_a_wait_that_gives_up_is_reported(cuda_lib):
+    """The first CTA of each cluster sends nothing: the others' waits run out, the status says so once, and a call after
+    it is right."""
+    import time
+    log_alpha, x, _ = draw((1, 4000, 100), torch.bfloat16, 81)
+    la, xd = log_alpha.cuda(), x.cuda()
+    assert cuda_lib.recurrence_status() == 0
+    torch.cuda.synchronize()
+    began = time.perf_counter()
+    cuda_lib.recurrence_timeout_test(la, xd, h=torch.empty_like(xd), wait_budget_cycles=1 << 20)
+    assert cuda_lib.recurrence_status() == 4
+    assert time.perf_counter() - began < 1.0
+    assert cuda_lib.recurrence_status() == 0
+    check_fwd(cuda_lib, log_alpha, x, None)
+    assert cuda_lib.recurrence_status() == 0
 
 
 @pytest.mark.parametrize("rows", [1, 6, 7, 14, 15, 16, 17, 34, 35, 74, 75, 148, 149])
