@@ -256,7 +256,7 @@ static bool dtype_ok(kda_dtype_t dtype) { return dtype == KDA_F32 || dtype == KD
 static bool good(const void* p) { return p != nullptr && aligned16(p); }
 
 static kda_status_t check_recurrence(const kda::RecurrenceArgs& a, kda_dtype_t dtype, bool bwd) {
-    if (a.N < 0 || a.T < 0 || a.D < 1) return KDA_ERR_INVALID_ARG;
+    if (a.N < 0 || a.T < 0 || a.D < 1 || a.D > 1 << 30) return KDA_ERR_INVALID_ARG;
     if (!dtype_ok(dtype)) return KDA_ERR_INVALID_ARG;
     if ((long long)a.N * ((a.D + 31) / 32) > 0x3ffffffLL) return KDA_ERR_INVALID_ARG;  // grid limit, clusters included
     if (a.cu_seqlens && (reinterpret_cast<uintptr_t>(a.cu_seqlens) & 3u) != 0) return KDA_ERR_INVALID_ARG;

@@ -7,18 +7,19 @@
 //
 // What bounds it: HBM. A context position costs 2 d elements of cache per
 // key-value head and 4 d flop per query head, so the products run on warp MMAs
-// (16 query heads x 16 positions; fewer heads leave rows empty, which costs
-// nothing while the loads set the pace).
+// (16 positions x 8 or 16 query heads; fewer heads leave columns empty, which
+// costs nothing while the loads set the pace). 64 rows of 256 to 16384 positions,
+// 8 key-value heads, d 128, bf16: 167-171 us, 0.94-0.96 of the measured copy
+// bandwidth, the tensor pipe 9 % busy.
 //
 // Split: the positions of all (sequence, key-value head, block of 16 query
 // heads) are cut into tiles of 16, and the list of all tiles is cut into equal
 // contiguous ranges, one per warp ("worker"), whatever the lengths are: a
 // batch of one long and many short contexts loads every SM alike. (To begin and
 // to end a pair costs as much as some tiles, so each pair counts kBegin more.)
-// Workers find
-// their range from seq_lens on the device. A worker that holds all tiles of a
-// pair writes its output; else it leaves (m, l, O) in the workspace, where it
-// has two places: 0 for a range that continues a pair, 1 for one that begins a
+// Workers find their range from seq_lens on the device. A worker that holds all
+// tiles of a pair writes its output; else it leaves (m, l, O) in the workspace,
+// where it has two places: 0 for a range that continues a pair, 1 for one that begins a
 // pair and does not end it. attn_join_kernel joins the pieces in order. A warp
 // works for itself (no block barrier in the loop): it copies 16 rows of K and V
 // a stage with 16-byte cp.async, several stages ahead, across the ends of pairs.
@@ -33,7 +34,7 @@ namespace {
 
 constexpr int kTile = 16;   // positions of a tile
 constexpr int kHeads = 16;  // query heads of a block
-constexpr int kBegin = 3;   // what a pair costs beside its tiles, in tiles
+constexpr int kBegin = 3;   // what a pair costs beside its tiles, in tiles (256 rows of 0 to 300: with 1 24.9 us, 3 21.4, 6 23.6)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // Stages of a worker's ring, workers of a CTA and CTAs of an SM: 190 to 220 KB

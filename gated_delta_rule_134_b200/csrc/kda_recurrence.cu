@@ -9,19 +9,21 @@
 // first: dx_t = dh_t + c, c <- a_t dx_t, dlog_alpha_t = c h_{t-1}.
 //
 // What bounds it: HBM, 3 (backward 5) elements of the tensors per token and
-// channel, each read or written once. One cluster of CTAs owns a (sequence,
-// slice of 128 bytes of channels) and walks the tokens, a tile of tokens per CTA
-// at a time. A thread has R consecutive tokens of 16 bytes of channels; it copies
-// them into shared memory two tiles ahead (it alone reads them back, so no
-// barrier is due) and then
+// channel, each read or written once. A row is a (sequence, slice of 128 bytes of
+// channels); one CTA walks its tokens, a tile at a time. A thread has kTokens
+// consecutive tokens of 16 bytes of channels; it copies them into shared memory
+// two tiles ahead (with 16-byte rows it alone reads them back, so no barrier is
+// due) and then
 //   1. composes its tokens into one span (A, H) and leaves it in shared memory;
 //   2. as (channel, part) composes the spans of one part of the CTA's token
-//      groups, then the parts' spans, and leaves the CTA's to the cluster;
-//   3. walks the CTAs and parts before its own, which gives the state that enters
-//      each of its groups, and leaves these in shared memory;
+//      groups, then the parts' spans;
+//   3. walks the parts before its own, which gives the state that enters each of
+//      its groups, and leaves these in shared memory;
 //   4. runs its tokens again from the state that enters them and writes them.
-// The sequential depth is T / (tokens of a cluster's tile). Nothing waits on a
-// flag, and the order of every product and sum is fixed by the sizes alone.
+// B4 T8192 D4096 bf16 takes 132-135 us (0.93 of the measured copy bandwidth), the
+// backward pass of B2 111-114 us (0.92). Where rows are few, a cluster of CTAs
+// shares one (recurrence_cluster_kernel). The order of every product and sum is
+// fixed by the sizes alone.
 #include "kda_async.cuh"
 #include "kda_common.cuh"
 #include "kda_internal.h"

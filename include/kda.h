@@ -356,7 +356,8 @@ kda_status_t kda_noalloc_status(void *stream);
  *                     kda_chunk_fwd_varlen (read on the device only, clamped
  *                     into [0, T]; tokens outside every sequence keep what h
  *                     held before)
- *   T >= 0, D >= 1 (any width; rows of 16-byte multiples are the fast case).
+ *   T >= 0, D in [1, 2^30] (any width; rows of 16-byte multiples are the fast
+ *   case).
  * An empty sequence copies h0 to h_T. State and sums in fp32; decays over
  * spans of tokens are exponentials of fp32 sums of log_alpha. Nothing depends
  * on timing: equal inputs give equal bits.

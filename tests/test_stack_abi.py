@@ -24,7 +24,7 @@ def rec_bwd(la=P[0], h=P[1], h0=None, dh=P[2], dT=None, dx=P[3], dla=P[4], d0=No
 
 
 @pytest.mark.parametrize("bad", [dict(la=None), dict(x=None), dict(h=None), dict(la=ODD), dict(x=ODD), dict(h=ODD), dict(h0=ODD),
-                                 dict(h_T=ODD), dict(cu=HALF), dict(N=-1), dict(T=-1), dict(D=0), dict(dtype=2), dict(N=1 << 30, D=4096)])
+                                 dict(h_T=ODD), dict(cu=HALF), dict(N=-1), dict(T=-1), dict(D=0), dict(dtype=2), dict(N=1 << 30, D=4096), dict(D=(1 << 30) + 1)])
 def test_recurrence_fwd_refuses(bad):
     assert rec_fwd(**bad) == 1
 
