@@ -272,9 +272,9 @@ struct Walk {
     // As (channel, part): channel p in the order of the spans, that is element e = 2 pair + half of thread column pcol.
     int p, part, pair, pcol, half, pc;
 
-    __device__ __forceinline__ Walk(const RecurrenceArgs& a_, long long id, int slices, int rank_, int size_) : a(a_), rank(rank_), size(size_) {
+    __device__ __forceinline__ Walk(const RecurrenceArgs& a_, int n_, long long id, int slices, int rank_, int size_)
+        : a(a_), rank(rank_), size(size_), n(n_) {
         const int tid = threadIdx.x;
-        n = (int)(id / slices);
         c0 = (int)(id % slices) * CT;
         D = a.D;
         token_range(a.cu_seqlens, n, a.T, begin, len);
@@ -425,6 +425,26 @@ struct Walk {
     }
 };
 
+// The k-th longest of N <= THREADS packed sequences: CTAs are given out in this order, so that no long sequence begins
+// when the others are done (nine sequences of 0 to 3400 tokens, D 2048: 46.7 us in the order they lie, 40.8 so).
+template <int THREADS> __device__ __forceinline__ int longest(const RecurrenceArgs& a, int k, int* scratch) {
+    const int i = threadIdx.x;
+    long long begin;
+    int len = -1;
+    if (i < a.N) {
+        token_range(a.cu_seqlens, i, a.T, begin, len);
+        scratch[i] = len;
+    }
+    __syncthreads();
+    int before = 0;
+    for (int j = 0; j < a.N; ++j) before += scratch[j] > len || (scratch[j] == len && j < i);
+    if (i < a.N && before == k) scratch[THREADS] = i;
+    __syncthreads();
+    const int n = scratch[THREADS];
+    __syncthreads();
+    return n;
+}
+
 // One CTA a row. R: tokens of a thread.
 template <typename T, int ALIGN, bool BWD, int R, int THREADS>
 __global__ void __launch_bounds__(THREADS, 512 / THREADS) recurrence_scan_kernel(RecurrenceArgs a, int slices) {
@@ -433,7 +453,9 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) recurrence_scan_kernel
     constexpr int V = Sm::V;
     extern __shared__ __align__(16) unsigned char smem[];
     const Sm sm(smem);
-    const Walk<T, ALIGN, BWD, R, THREADS, Sm> walk(a, blockIdx.x, slices, 0, 1);
+    int n = blockIdx.x / slices;
+    if (a.cu_seqlens && a.N > 1 && a.N <= THREADS) n = longest<THREADS>(a, n, reinterpret_cast<int*>(sm.spans));
+    const Walk<T, ALIGN, BWD, R, THREADS, Sm> walk(a, n, blockIdx.x, slices, 0, 1);
     float state = walk.first_state();  // every part keeps its channel's, by the same operations
     const int tiles = walk.tiles();
     for (int k = 0; k < S; ++k) {
@@ -495,16 +517,15 @@ __device__ __forceinline__ void push(const void* to, uint64_t* bar, int rank, fl
 // met in a.wait_cycles sets g_recurrence_late, and the kernel ends without waiting, pushing or arming a barrier again (the
 // others' next waits then give up too). An inbox slot is written again two tiles later, when its owner has sent the tile
 // between, which it does after having read the slot and armed its barrier again.
-template <typename T, int ALIGN, bool BWD, int R, int THREADS>
+template <typename T, int ALIGN, bool BWD, int R, int THREADS, int S>
 __global__ void __launch_bounds__(THREADS, 1) recurrence_cluster_kernel(RecurrenceArgs a, int slices) {
-    constexpr int S = 4;
     using Sm = ScanSmem<T, R, THREADS, S, 2>;
     constexpr int V = Sm::V, CT = Sm::CT;
     extern __shared__ __align__(16) unsigned char smem[];
     const Sm sm(smem);
     const cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank(), size = (int)cluster.num_blocks();
-    const Walk<T, ALIGN, BWD, R, THREADS, Sm> walk(a, blockIdx.x / size, slices, rank, size);
+    const Walk<T, ALIGN, BWD, R, THREADS, Sm> walk(a, blockIdx.x / size / slices, blockIdx.x / size, slices, rank, size);
     float state = walk.first_state();
     float2* inbox = sm.whole;  // [parity][rank][channel]: the CTAs' spans
     uint64_t* bar = reinterpret_cast<uint64_t*>(inbox + 2 * kMaxCluster * CT);  // [parity]: they have arrived
@@ -654,12 +675,17 @@ cudaError_t launch_rows(const RecurrenceArgs& a, int slices, cudaStream_t stream
     return cudaGetLastError();
 }
 
+// A thread's tokens in a cluster. Eight of a float row fill as many registers as four of a bf16 one and halve the rounds:
+// T16384 D1000 39 us, with four 44. Not so where a thread has the backward pass's h beside them (82 and 67) or copies by
+// words (T16384 D1001 102 and 60).
+template <typename T, int ALIGN, bool BWD> constexpr int cluster_tokens() { return sizeof(T) == 4 && ALIGN == 16 && !BWD ? 8 : 4; }
+
 template <typename T, int ALIGN, bool BWD>
 cudaError_t launch_clusters(const RecurrenceArgs& a, int slices, int size, cudaStream_t stream) {
-    constexpr int THREADS = 256;
-    using Sm = ScanSmem<T, kTokens, THREADS, 4, 2>;
+    constexpr int THREADS = 256, R = cluster_tokens<T, ALIGN, BWD>(), S = R == 4 ? 4 : 3;
+    using Sm = ScanSmem<T, R, THREADS, S, 2>;
     constexpr int kBytes = Sm::kBytes + 2 * kMaxCluster * Sm::CT * (int)sizeof(float2) + 16;
-    auto kernel = recurrence_cluster_kernel<T, ALIGN, BWD, kTokens, THREADS>;
+    auto kernel = recurrence_cluster_kernel<T, ALIGN, BWD, R, THREADS, S>;
     static std::atomic<unsigned long long> raised{0};
     cudaError_t err = size > 8 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) : cudaSuccess;
     if (err == cudaSuccess) err = allow_smem(kernel, kBytes, raised);
@@ -691,7 +717,7 @@ cudaError_t launch_scan(const RecurrenceArgs& a, cudaStream_t stream) {
     // rounds (T 32768: 82 us, with four 97). No more than the tokens give tiles to.
     const int most = rows <= 6 ? 16 : rows <= 14 ? 8 : rows <= 16 ? 16 : rows <= 34 ? 4 : rows < 75 ? 2 : 1;
     int size = 1;
-    while (size < most && (long long)size * (256 / 8) * kTokens < tokens) size *= 2;
+    while (size < most && (long long)size * (256 / 8) * cluster_tokens<T, ALIGN, BWD>() < tokens) size *= 2;
     if (a.test_withhold && size == 1) return cudaErrorInvalidValue;
     if (size > 1) return launch_clusters<T, ALIGN, BWD>(a, slices, size, stream);
     // One CTA of 512 threads on an SM takes tiles of twice the tokens, and its SM's share of the bandwidth with fewer

@@ -82,6 +82,26 @@ def test_packed(cuda_lib, dtype, D, lens):
     check_bwd(cuda_lib, log_alpha, h.cpu(), h0, dh, dT, cu)
 
 
+@pytest.mark.parametrize("lens", [[700, 0, 1500, 20, 900], [600, 600, 600, 600, 600]])
+def test_packed_many_rows(cuda_lib, lens):
+    """Rows enough for one large CTA each, the longest sequences first, ties among them."""
+    T, N, D = sum(lens), len(lens), 1000
+    log_alpha, x, g = draw((T, D), torch.bfloat16, 4 + T)
+    cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32)
+    h0 = torch.randn(N, D, generator=g)
+    h, _ = check_fwd(cuda_lib, log_alpha, x, h0, cu)
+    check_bwd(cuda_lib, log_alpha, h.cpu(), h0, x, h0, cu)
+
+
+def test_packed_more_sequences_than_threads(cuda_lib):
+    g = torch.Generator().manual_seed(6)
+    lens = torch.randint(0, 12, (700,), generator=g).tolist()
+    T = sum(lens)
+    log_alpha, x, g = draw((T, 24), torch.float32, 7)
+    cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32)
+    check_fwd(cuda_lib, log_alpha, x, torch.randn(700, 24, generator=g), cu)
+
+
 def test_packed_equals_dense_bits(cuda_lib):
     log_alpha, x, g = draw((3, 200, 72), torch.bfloat16, 5)
     h0 = torch.randn(3, 72, generator=g).cuda()
