@@ -26,6 +26,7 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr long long kBwdCtas = 296;  // of the backward pass: two on each of 148 SMs
 enum { kNoTurn = 0, kHalves = 1, kPairs = 2 };
 
 // One side (queries or keys) of a call.
@@ -267,8 +268,8 @@ __global__ void __launch_bounds__(kThreads) qk_fwd_kernel(QkArgs a, int chunk, i
 // pairs of channels (one instruction for two products), without which the kernel would be bound by its instructions.
 template <typename T> struct BwdPlan {
     static constexpr int kRowBytes = 8 * sizeof(T);                 // a thread's channels of one head
-    static constexpr int kStages = 8 / (sizeof(T) / 2);             // heads in flight
-    static constexpr int kSmem = kStages * 2 * kRowBytes * kThreads;  // 64 KB
+    static constexpr int kStages = sizeof(T) == 2 ? 6 : 4;           // heads in flight (bf16: with 8 or 12 it is 2 to 4 % slower)
+    static constexpr int kSmem = kStages * 2 * kRowBytes * kThreads;  // 48 or 64 KB
 };
 
 template <typename T, int LANES, int MODE>
@@ -442,15 +443,17 @@ __global__ void __launch_bounds__(1024) qk_dw_kernel(const float* part, float* d
     const int x = threadIdx.x & 31, y = threadIdx.x >> 5, c = blockIdx.y * 32 + x;
     const int b = blockIdx.x == 0 ? 0 : q_ctas, e = blockIdx.x == 0 ? q_ctas : ctas;
     float sum = 0.f;
-    if (c < d)
-        for (int i = b + y; i < e; i += 32) sum += part[(size_t)i * d + c];
+#pragma unroll
+    for (int k = 0; k < (int)(kBwdCtas + 31) / 32; ++k) {  // all loads at once
+        const int i = b + y + 32 * k;
+        sum += c < d && i < e ? part[(size_t)i * d + c] : 0.f;
+    }
     s[y][x] = sum;
     __syncthreads();
     sum = warp_sum(s[x][y]);  // channel y of the block
     if (x == 0 && blockIdx.y * 32 + y < d) dw[blockIdx.y * 32 + y] = sum;
 }
 
-constexpr long long kBwdCtas = 296;  // two on each of 148 SMs
 
 template <typename F> cudaError_t with_lanes(int d, F f) {
     if (d <= 8) return f(std::integral_constant<int, 1>());
