@@ -88,9 +88,10 @@ template <typename T, int ALIGN> __device__ __forceinline__ int channel_of(int c
     return ALIGN == 16 ? col * V + e : (col + 8 * (e / P)) * P + e % P;
 }
 
-__device__ __forceinline__ void cp_async4(void* dst, const void* src, bool on) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
-                 "l"(src), "r"(on ? 4 : 0)
+// At most `bytes` of the 16 at `src`, zeros for the rest.
+__device__ __forceinline__ void cp_async16_some(void* dst, const void* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+                 "l"(src), "r"(bytes)
                  : "memory");
 }
 
@@ -119,84 +120,51 @@ __device__ __forceinline__ Pack<T> read_row(const T* row, int c0, int col, int D
     return r;
 }
 
-// Stage `slot` ([token of the tile][32 words], then one more word a token) gets this warp's 4 R tokens of one tensor,
-// without waiting. `first`: the row of the CTA's first token; `step`: from a token to the next (D or -D); `left`: the
-// number of tokens there are. With 16-byte rows every thread copies what it will read; else a warp copies one token's 32
-// words at a time, because copies that touch four rows at once are bound by the load unit (the readers then need
-// __syncwarp). Words are swizzled by token group, so that the four groups of a warp read different banks. Rows that
-// begin in the middle of a word (ALIGN 2, every other row) are copied from that word on, 33 words, and shifted by the
-// reader; a word that reaches past the tensor's end `stop` is read by halves.
+// The bytes of one tensor's tile in shared memory. With 16-byte rows: [token of a thread][thread], 16 bytes each. Else
+// every token has the nine 16-byte pieces that its 128 bytes may touch; the token groups lie 32 bytes further apart, so
+// that the four of a warp read different banks.
+constexpr int kRowPieces = 9;
+template <int ALIGN, int R> constexpr int group_bytes() { return ALIGN == 16 ? R * 8 * 16 : R * kRowPieces * 16 + 32; }
+
+// Copies this warp's 4 R tokens of one tensor into its tile, without waiting. `first`: the row of the CTA's first token;
+// `step`: from a token to the next (D or -D); `left`: the number of tokens there are; tokens past them become zeros. With
+// 16-byte rows every thread copies what it will read; else the lanes share the pieces of all rows, begin each row at the
+// 16 bytes that hold its first element, and stop at the tensor's end (the readers then need __syncwarp).
 template <typename T, int ALIGN, int R, int THREADS>
-__device__ __forceinline__ void copy_tile(uint32_t* slot, const T* first, int step, int left, int c0, int D, const T* stop) {
-    constexpr int P = 4 / sizeof(T);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = lane & 7;
+__device__ __forceinline__ void copy_tile(unsigned char* slot, const T* first, int step, int left, int c0, int D, const T* stop) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if constexpr (ALIGN == 16) {
-        const int k0 = (threadIdx.x >> 3) * R, c = c0 + col * Pack<T>::V;
+        const int k0 = (threadIdx.x >> 3) * R, c = c0 + (lane & 7) * Pack<T>::V;
 #pragma unroll
         for (int i = 0; i < R; ++i)
-            cp_async16(reinterpret_cast<uint4*>(slot) + i * THREADS + threadIdx.x, first + (long long)(k0 + i) * step + c,
-                       k0 + i < left && c < D);
-        return;
-    }
-    const int k0 = warp * 4 * R;
-    uint32_t* to = slot + k0 * 32;
-    left -= k0;
-    if constexpr (ALIGN == 4) {
-        const int c = c0 + lane * P;
-        if (c >= D) left = 0;
-        const T* row = first + (long long)k0 * step + c;
-#pragma unroll
-        for (int k = 0; k < 4 * R; ++k, row += step) cp_async4(to + k * 32 + (lane ^ (8 * (k / R))), row, k < left);
+            cp_async16(slot + (i * THREADS + threadIdx.x) * 16, first + (long long)(k0 + i) * step + c, k0 + i < left && c < D);
     } else {
-        const int n = min(D - c0, 64);
-        const char* at = reinterpret_cast<const char*>(first + (long long)k0 * step + c0);
-        // the word that holds the tensor's last element may lie in this warp's rows
-        const char* last = step > 0 ? at + 2ll * step * (min(left, 4 * R) - 1) : at;
-        const bool ends = left > 0 && last + 4 * 33 > reinterpret_cast<const char*>(stop);
-        const int left0 = 2 * lane < n ? left : 0, left1 = 2 * lane - 1 < n ? left : 0;  // rows that need this lane's word
-        {
-            const char* mine = at + 2ll * step * lane;  // lane k: the 33rd word of row k
-            if (lane < 4 * R && (reinterpret_cast<uintptr_t>(mine) & 2)) {
-                const char* w = mine - 2 + 128;
-                const bool on = lane < left && n == 64;
-                uint32_t* dst = slot + THREADS / 8 * R * 32 + k0 + lane;
-                if (on && w + 4 > reinterpret_cast<const char*>(stop)) *dst = *reinterpret_cast<const unsigned short*>(w);
-                else cp_async4(dst, w, on);
-            }
-        }
-        if (!ends) {
+        const int bytes = min(D - c0, (int)(128 / sizeof(T))) * (int)sizeof(T);
+        const char* base = reinterpret_cast<const char*>(first + (long long)warp * 4 * R * step + c0);
+        left -= warp * 4 * R;
+        unsigned char* to = slot + warp * 4 * group_bytes<ALIGN, R>();
 #pragma unroll
-            for (int k = 0; k < 4 * R; ++k, at += 2ll * step) {
-                const uintptr_t w = reinterpret_cast<uintptr_t>(at);
-                cp_async4(to + k * 32 + (lane ^ (8 * (k / R))), reinterpret_cast<const char*>(w & ~(uintptr_t)2) + 4 * lane,
-                          k < (w & 2 ? left1 : left0));
-            }
-        } else {
-#pragma unroll 1
-            for (int k = 0; k < 4 * R; ++k, at += 2ll * step) {
-                const uintptr_t w = reinterpret_cast<uintptr_t>(at);
-                const char* from = reinterpret_cast<const char*>(w & ~(uintptr_t)2) + 4 * lane;
-                const bool on = k < (w & 2 ? left1 : left0);
-                uint32_t* dst = to + k * 32 + (lane ^ (8 * (k / R)));
-                if (on && from + 4 > reinterpret_cast<const char*>(stop)) *dst = *reinterpret_cast<const unsigned short*>(from);
-                else cp_async4(dst, from, on);
-            }
+        for (int j = 0; j < (4 * R * kRowPieces + 31) / 32; ++j) {
+            const int q = j * 32 + lane, k = q / kRowPieces, piece = q % kRowPieces;
+            if (4 * R * kRowPieces % 32 != 0 && k >= 4 * R) continue;
+            const uintptr_t row = reinterpret_cast<uintptr_t>(base + (long long)k * step * (int)sizeof(T));
+            const char* from = reinterpret_cast<const char*>(row & ~(uintptr_t)15) + piece * 16;
+            const bool on = k < left && piece * 16 < (int)(row & 15) + bytes;
+            const long long there = reinterpret_cast<const char*>(stop) - from;
+            cp_async16_some(to + (k / R) * group_bytes<ALIGN, R>() + (k % R * kRowPieces + piece) * 16, from, on ? (int)min(there, 16ll) : 0);
         }
     }
 }
-// This thread's channels of its token i; `odd`: the row begins in the middle of a word.
-template <typename T, int ALIGN, int R, int THREADS> __device__ __forceinline__ Pack<T> slot_of(const uint32_t* slot, int i, bool odd) {
+// This thread's channels of its token i; `off`: the row's first byte modulo 16.
+template <typename T, int ALIGN, int R, int THREADS> __device__ __forceinline__ Pack<T> slot_of(const unsigned char* slot, int i, int off) {
     if constexpr (ALIGN == 16) return Pack<T>::of(reinterpret_cast<const uint4*>(slot)[i * THREADS + threadIdx.x]);
-    const int col = threadIdx.x & 7, group = threadIdx.x >> 3, turn = 8 * (group & 3);
-    const uint32_t* at = slot + (group * R + i) * 32;
+    const int col = threadIdx.x & 7, group = threadIdx.x >> 3;
+    const uint32_t* at = reinterpret_cast<const uint32_t*>(slot + group * group_bytes<ALIGN, R>() + i * kRowPieces * 16) + (off >> 2) + col;
     Pack<T> r;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const int k = col + 8 * j;
-        r.w[j] = at[k ^ turn];
-        if constexpr (ALIGN == 2) {
-            if (odd) r.w[j] = __funnelshift_r(r.w[j], k == 31 ? slot[THREADS / 8 * R * 32 + group * R + i] : at[(k + 1) ^ turn], 16);
-        }
+        r.w[j] = at[8 * j];
+        if constexpr (ALIGN == 2) r.w[j] = __funnelshift_r(r.w[j], at[8 * j + 1], off & 2 ? 16 : 0);
     }
     return r;
 }
@@ -235,29 +203,29 @@ __device__ __forceinline__ void store_row(T* row, int c0, int col, int D, const 
 
 // Sizes, and shared memory: the ring of STAGES stages, the spans of the token groups, the states that enter them
 // (STATES copies), the spans of the CTA's parts, and the CTA's span by parity of the tile.
-template <typename T, int R, int THREADS, int STAGES, int STATES> struct ScanSmem {
+template <typename T, int ALIGN, int R, int THREADS, int STAGES, int STATES> struct ScanSmem {
     static constexpr int V = Pack<T>::V, CT = 8 * V;        // channels of a thread, of a slice
     static constexpr int kGroups = THREADS / 8;            // token groups of a CTA (8 threads across the channels)
     static constexpr int kTile = kGroups * R;              // tokens
     static constexpr int kParts = THREADS / CT, kPer = kGroups / kParts;
-    static constexpr int kSlot = R * THREADS * 16 + kGroups * R * 4;  // one tensor's tile, and a word more a token
+    static constexpr int kSlot = kGroups * group_bytes<ALIGN, R>();  // one tensor's tile
     static constexpr int kStage = 2 * kSlot;
     static constexpr int kSpans = kGroups * CT * (int)sizeof(float2), kStates = kGroups * CT * (int)sizeof(float);
     static constexpr int kBytes = STAGES * kStage + kSpans + STATES * kStates + kParts * CT * (int)sizeof(float2);
 
-    uint32_t* ring;
+    unsigned char* ring;
     float4* spans;      // [group][pair of V/2][col]: A, H, A, H
     float* states;      // [copy][group][quad of V/4][col][4]
     float2* parts;      // [part][channel]
     float2* whole;      // what follows
     __device__ __forceinline__ explicit ScanSmem(unsigned char* smem) {
-        ring = reinterpret_cast<uint32_t*>(smem);
+        ring = smem;
         spans = reinterpret_cast<float4*>(smem + STAGES * kStage);
         states = reinterpret_cast<float*>(smem + STAGES * kStage + kSpans);
         parts = reinterpret_cast<float2*>(smem + STAGES * kStage + kSpans + STATES * kStates);
         whole = parts + kParts * CT;
     }
-    __device__ __forceinline__ uint32_t* stage(int k) const { return ring + k * (kStage / 4); }
+    __device__ __forceinline__ unsigned char* stage(int k) const { return ring + k * kStage; }
 };
 
 // What a thread knows of its sequence and slice, and the steps that both scan kernels take.
@@ -283,7 +251,7 @@ struct Walk {
         hf = BWD ? (const T*)a.h_fwd + begin * D : nullptr;
         out = (T*)a.out + begin * D;
         out_la = BWD ? (T*)a.out_la + begin * D : nullptr;
-        const long long cells = (a.cu_seqlens ? 1ll : (long long)a.N) * a.T * D;  // the end of the tensors, for ALIGN 2
+        const long long cells = (a.cu_seqlens ? 1ll : (long long)a.N) * a.T * D;  // the end of the tensors
         la_stop = (const T*)a.log_alpha + cells;
         x_stop = (const T*)a.x + cells;
         col = tid & 7;
@@ -310,21 +278,19 @@ struct Walk {
         const unsigned at = number(tile, group * R + i);
         return at < (unsigned)len ? (BWD ? len - 1 - (int)at : (int)at) : -1;
     }
-    __device__ __forceinline__ void fetch(uint32_t* to, int tile) const {
+    __device__ __forceinline__ void fetch(unsigned char* to, int tile) const {
         const long long at = number(tile, 0);
         const int left = (int)min(max(len - at, 0ll), (long long)Sm::kTile);
         const long long row = (BWD ? len - 1 - at : at) * D;
         copy_tile<T, ALIGN, R, THREADS>(to, la + row, BWD ? -D : D, left, c0, D, la_stop);
-        copy_tile<T, ALIGN, R, THREADS>(to + Sm::kSlot / 4, x + row, BWD ? -D : D, left, c0, D, x_stop);
+        copy_tile<T, ALIGN, R, THREADS>(to + Sm::kSlot, x + row, BWD ? -D : D, left, c0, D, x_stop);
     }
     // Token i of a fetched tile.
-    __device__ __forceinline__ void read(const uint32_t* from, int tile, int i, Pack<T>& pl, Pack<T>& px) const {
-        // D is odd and the tensors begin on 16 bytes: every other row begins in the middle of a word
-        // (those past the end, which hold zeros, counted on: the copy goes by the same rows)
-        const unsigned at = number(tile, group * R + i);
-        const bool odd = ALIGN == 2 && (((unsigned)begin + (BWD ? len - 1 - at : at)) & 1);
-        pl = slot_of<T, ALIGN, R, THREADS>(from, i, odd);
-        px = slot_of<T, ALIGN, R, THREADS>(from + Sm::kSlot / 4, i, odd);
+    __device__ __forceinline__ void read(const unsigned char* from, int tile, int i, Pack<T>& pl, Pack<T>& px) const {
+        // the tensors and the slices begin on 16 bytes, so both rows begin alike (past the end are zeros, wherever read)
+        const int off = ALIGN == 16 ? 0 : (int)(((unsigned)begin + (unsigned)token(tile, i)) * (unsigned)D * (unsigned)sizeof(T) & 15u);
+        pl = slot_of<T, ALIGN, R, THREADS>(from, i, off);
+        px = slot_of<T, ALIGN, R, THREADS>(from + Sm::kSlot, i, off);
     }
     // h_{t-1} of the thread's tokens (zeros for the first token, whose is h0)
     __device__ __forceinline__ void read_before(int tile, Pack<T> (&ph)[R]) const {
@@ -449,7 +415,7 @@ template <int THREADS> __device__ __forceinline__ int longest(const RecurrenceAr
 template <typename T, int ALIGN, bool BWD, int R, int THREADS>
 __global__ void __launch_bounds__(THREADS, 512 / THREADS) recurrence_scan_kernel(RecurrenceArgs a, int slices) {
     constexpr int S = 2;
-    using Sm = ScanSmem<T, R, THREADS, S, 1>;
+    using Sm = ScanSmem<T, ALIGN, R, THREADS, S, 1>;
     constexpr int V = Sm::V;
     extern __shared__ __align__(16) unsigned char smem[];
     const Sm sm(smem);
@@ -519,7 +485,7 @@ __device__ __forceinline__ void push(const void* to, uint64_t* bar, int rank, fl
 // between, which it does after having read the slot and armed its barrier again.
 template <typename T, int ALIGN, bool BWD, int R, int THREADS, int S>
 __global__ void __launch_bounds__(THREADS, 1) recurrence_cluster_kernel(RecurrenceArgs a, int slices) {
-    using Sm = ScanSmem<T, R, THREADS, S, 2>;
+    using Sm = ScanSmem<T, ALIGN, R, THREADS, S, 2>;
     constexpr int V = Sm::V, CT = Sm::CT;
     extern __shared__ __align__(16) unsigned char smem[];
     const Sm sm(smem);
@@ -666,7 +632,7 @@ __global__ void __launch_bounds__(256) recurrence_step_kernel(const T* log_alpha
 
 template <typename T, int ALIGN, bool BWD, int THREADS>
 cudaError_t launch_rows(const RecurrenceArgs& a, int slices, cudaStream_t stream) {
-    using Sm = ScanSmem<T, kTokens, THREADS, 2, 1>;
+    using Sm = ScanSmem<T, ALIGN, kTokens, THREADS, 2, 1>;
     auto kernel = recurrence_scan_kernel<T, ALIGN, BWD, kTokens, THREADS>;
     static std::atomic<unsigned long long> raised{0};
     const cudaError_t err = allow_smem(kernel, Sm::kBytes, raised);
@@ -683,7 +649,7 @@ template <typename T, int ALIGN, bool BWD> constexpr int cluster_tokens() { retu
 template <typename T, int ALIGN, bool BWD>
 cudaError_t launch_clusters(const RecurrenceArgs& a, int slices, int size, cudaStream_t stream) {
     constexpr int THREADS = 256, R = cluster_tokens<T, ALIGN, BWD>(), S = R == 4 ? 4 : 3;
-    using Sm = ScanSmem<T, R, THREADS, S, 2>;
+    using Sm = ScanSmem<T, ALIGN, R, THREADS, S, 2>;
     constexpr int kBytes = Sm::kBytes + 2 * kMaxCluster * Sm::CT * (int)sizeof(float2) + 16;
     auto kernel = recurrence_cluster_kernel<T, ALIGN, BWD, R, THREADS, S>;
     static std::atomic<unsigned long long> raised{0};
