@@ -95,29 +95,56 @@ __device__ __forceinline__ void cp_async16_some(void* dst, const void* src, int 
                  : "memory");
 }
 
-// One row's channels of this thread; zeros where `on` is false or past the last channel.
+// One row's channels of this thread as row_of returns them; zeros where `on` is false or past the last channel. Loading
+// and shifting are apart, so that the loads can be under way. Rows that are even in 2-byte elements alone are read by the
+// words that lie on 4 bytes: where the row begins within such a word, the thread has the second half of what it needs
+// from the next lane, the last lane's very last from a load of its own. (By 2-byte loads and stores the backward pass of
+// T16384 D1001 bf16 takes 251 us, so 149; the forward pass 94 and 84.)
+template <typename T, int ALIGN> struct RowWords {
+    Pack<T> p;
+    uint32_t last;
+};
 template <typename T, int ALIGN>
-__device__ __forceinline__ Pack<T> read_row(const T* row, int c0, int col, int D, bool on) {
+__device__ __forceinline__ RowWords<T, ALIGN> read_row(const T* row, int c0, int col, int D, bool on) {
     constexpr int P = 4 / sizeof(T);
-    Pack<T> r;
-    r.w[0] = r.w[1] = r.w[2] = r.w[3] = 0u;
+    RowWords<T, ALIGN> r;
+    r.p.w[0] = r.p.w[1] = r.p.w[2] = r.p.w[3] = r.last = 0u;
     if constexpr (ALIGN == 16) {
         const int c = c0 + col * Pack<T>::V;
-        if (on && c < D) r = Pack<T>::of(__ldcs(reinterpret_cast<const uint4*>(row + c)));
+        if (on && c < D) r.p = Pack<T>::of(__ldcs(reinterpret_cast<const uint4*>(row + c)));
     } else if constexpr (ALIGN == 4) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int c = c0 + (col + 8 * j) * P;
-            if (on && c < D) r.w[j] = __ldcs(reinterpret_cast<const unsigned*>(row + c));
+            if (on && c < D) r.p.w[j] = __ldcs(reinterpret_cast<const unsigned*>(row + c));
         }
     } else {
+        // the tensor begins on 4 bytes: a row that does not has an element before it
+        const int odd = (int)(reinterpret_cast<uintptr_t>(row) >> 1 & 1);
+        const unsigned short* half = reinterpret_cast<const unsigned short*>(row);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int c = c0 + channel_of<T, ALIGN>(col, e);
-            if (on && c < D) r.w[e >> 1] |= (uint32_t)__ldcs(reinterpret_cast<const unsigned short*>(row) + c) << (e & 1 ? 16 : 0);
+        for (int j = 0; j < 4; ++j) {
+            const int c = c0 + (col + 8 * j) * P - odd;
+            if (on && c + 1 < D) r.p.w[j] = __ldcs(reinterpret_cast<const unsigned*>(half + c));
+            else if (on && c < D) r.p.w[j] = __ldcs(half + c);
         }
+        if (on && odd && col == 7 && c0 + 63 < D) r.last = __ldcs(half + c0 + 63);
     }
     return r;
+}
+// Called by all lanes.
+template <typename T, int ALIGN> __device__ __forceinline__ Pack<T> row_of(const RowWords<T, ALIGN>& r, const T* row, int col) {
+    if constexpr (ALIGN != 2) return r.p;
+    const int shift = (int)(reinterpret_cast<uintptr_t>(row) & 2) * 8;
+    Pack<T> p;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t give = col == 0 ? (j < 3 ? r.p.w[(j + 1) & 3] : 0u) : r.p.w[j];
+        uint32_t next = __shfl_sync(0xffffffffu, give, (col + 1) & 7, 8);
+        if (j == 3 && col == 7) next = r.last;
+        p.w[j] = __funnelshift_r(r.p.w[j], next, shift);
+    }
+    return p;
 }
 
 // The bytes of one tensor's tile in shared memory. With 16-byte rows: [token of a thread][thread], 16 bytes each. Else
@@ -169,35 +196,43 @@ template <typename T, int ALIGN, int R, int THREADS> __device__ __forceinline__ 
     return r;
 }
 
+// Writes this thread's channels of a row, where `on`. Called by all lanes.
 template <typename T, int ALIGN>
-__device__ __forceinline__ void store_row(T* row, int c0, int col, int D, const float (&x)[Pack<T>::V]) {
+__device__ __forceinline__ void store_row(T* row, int c0, int col, int D, bool on, const float (&x)[Pack<T>::V]) {
     constexpr int V = Pack<T>::V, P = 4 / sizeof(T);
-    if constexpr (ALIGN == 2) {
+    uint32_t w[4];
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            const int c = c0 + channel_of<T, ALIGN>(col, e);
-            if (c < D) row[c] = from_f32<T>(x[e]);
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (V == 4) {
+            w[i] = __float_as_uint(x[i]);
+        } else {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+    }
+    if constexpr (ALIGN == 16) {
+        if (on && c0 + col * V < D) __stcs(reinterpret_cast<uint4*>(row + c0 + col * V), make_uint4(w[0], w[1], w[2], w[3]));
+    } else if constexpr (ALIGN == 4) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int c = c0 + (col + 8 * j) * P;
+            if (on && c < D) *reinterpret_cast<uint32_t*>(row + c) = w[j];
         }
     } else {
-        uint32_t w[4];
+        const int odd = (int)(reinterpret_cast<uintptr_t>(row) >> 1 & 1);
+        unsigned short* half = reinterpret_cast<unsigned short*>(row);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if constexpr (V == 4) {
-                w[i] = __float_as_uint(x[i]);
-            } else {
-                const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-                w[i] = *reinterpret_cast<const uint32_t*>(&b);
-            }
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t give = col == 7 ? (j > 0 ? w[(j + 3) & 3] : 0u) : w[j];
+            const uint32_t before = __shfl_sync(0xffffffffu, give, (col + 7) & 7, 8);
+            const uint32_t v = odd ? __funnelshift_l(before, w[j], 16) : w[j];
+            const int c = c0 + (col + 8 * j) * P - odd;
+            if (!on || c >= D) continue;
+            if (c < c0) half[c0] = (unsigned short)(v >> 16);  // the word's first half is another slice's or row's
+            else if (c + 1 < D) *reinterpret_cast<uint32_t*>(half + c) = v;
+            else half[c] = (unsigned short)v;
         }
-        if constexpr (ALIGN == 16) {
-            if (c0 + col * V < D) __stcs(reinterpret_cast<uint4*>(row + c0 + col * V), make_uint4(w[0], w[1], w[2], w[3]));
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int c = c0 + (col + 8 * j) * P;
-                if (c < D) *reinterpret_cast<uint32_t*>(row + c) = w[j];
-            }
-        }
+        if (on && odd && col == 7 && c0 + 63 < D) half[c0 + 63] = (unsigned short)(w[3] >> 16);
     }
 }
 
@@ -292,12 +327,13 @@ struct Walk {
         pl = slot_of<T, ALIGN, R, THREADS>(from, i, off);
         px = slot_of<T, ALIGN, R, THREADS>(from + Sm::kSlot, i, off);
     }
+    __device__ __forceinline__ const T* before(int t) const { return hf + (long long)max(t - 1, 0) * D; }
     // h_{t-1} of the thread's tokens (zeros for the first token, whose is h0)
-    __device__ __forceinline__ void read_before(int tile, Pack<T> (&ph)[R]) const {
+    __device__ __forceinline__ void read_before(int tile, RowWords<T, ALIGN> (&ph)[R]) const {
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             const int t = token(tile, i);
-            ph[i] = read_row<T, ALIGN>(hf + (long long)max(t - 1, 0) * D, c0, col, D, t > 0);
+            ph[i] = read_row<T, ALIGN>(before(t), c0, col, D, t > 0);
         }
     }
     __device__ __forceinline__ static void decays(const Pack<T>& pl, F2 (&d)[V / 2]) {
@@ -358,8 +394,11 @@ struct Walk {
         }
     }
     // Token i from the state that enters it: writes its outputs, moves the state on.
-    __device__ __forceinline__ void run_token(int tile, int i, const F2 (&d)[V / 2], const Pack<T>& px, const Pack<T>& ph, F2 (&cur)[V / 2]) const {
+    __device__ __forceinline__ void run_token(int tile, int i, const F2 (&d)[V / 2], const Pack<T>& px, const RowWords<T, ALIGN>& words,
+                                              F2 (&cur)[V / 2]) const {
         const int t = token(tile, i);
+        Pack<T> ph;
+        if constexpr (BWD) ph = row_of<T, ALIGN>(words, before(t), col);
         float y[V], z[V];
 #pragma unroll
         for (int e = 0; e < V / 2; ++e) {
@@ -384,10 +423,8 @@ struct Walk {
             y[2 * e] = yy.x;
             y[2 * e + 1] = yy.y;
         }
-        if (t >= 0) {
-            store_row<T, ALIGN>(out + (long long)t * D, c0, col, D, y);
-            if constexpr (BWD) store_row<T, ALIGN>(out_la + (long long)t * D, c0, col, D, z);
-        }
+        store_row<T, ALIGN>(out + (long long)t * D, c0, col, D, t >= 0, y);
+        if constexpr (BWD) store_row<T, ALIGN>(out_la + (long long)t * D, c0, col, D, t >= 0, z);
     }
 };
 
@@ -433,7 +470,8 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) recurrence_scan_kernel
         cp_async_wait<S - 1>();
         if constexpr (ALIGN != 16) __syncwarp();
         F2 d[R][V / 2], A[V / 2], H[V / 2];
-        Pack<T> px[R], ph[R];
+        Pack<T> px[R];
+        RowWords<T, ALIGN> ph[R];
         if constexpr (BWD) walk.read_before(tile, ph);  // used at the tile's end
 #pragma unroll
         for (int i = 0; i < R; ++i) {
@@ -552,7 +590,7 @@ __global__ void __launch_bounds__(THREADS, 1) recurrence_cluster_kernel(Recurren
 #pragma unroll
             for (int e = 0; e < V / 2; ++e) d[i][e] = d1[i][e];
         }
-        Pack<T> ph[R];
+        RowWords<T, ALIGN> ph[R];
         if constexpr (BWD) walk.read_before(tile, ph);
         F2 A[V / 2], H[V / 2];
         if (more) {
