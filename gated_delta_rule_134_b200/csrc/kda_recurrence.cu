@@ -680,8 +680,8 @@ cudaError_t launch_rows(const RecurrenceArgs& a, int slices, cudaStream_t stream
 }
 
 // A thread's tokens in a cluster. Eight of a float row fill as many registers as four of a bf16 one and halve the rounds:
-// T16384 D1000 39 us, with four 44. Not so where a thread has the backward pass's h beside them (82 and 67) or copies by
-// words (T16384 D1001 102 and 60).
+// T16384 D1000 39 us, with four 44. Not so where a thread has the backward pass's h beside them (82 and 67); for unaligned
+// rows eight leave no room for a third stage, and six take 63 us where four take 59.
 template <typename T, int ALIGN, bool BWD> constexpr int cluster_tokens() { return sizeof(T) == 4 && ALIGN == 16 && !BWD ? 8 : 4; }
 
 template <typename T, int ALIGN, bool BWD>
