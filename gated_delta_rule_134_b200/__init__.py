@@ -446,6 +446,27 @@ def noalloc_status(device=None, stream=None) -> int:
         return int(load().kda_noalloc_status(_stream(stream, dev)))
 
 
+# ---------------------------------------------------------------- what the stack's other layers share
+
+
+def _memory_of(stream):
+    """Outputs and workspaces that a call allocates belong to the stream its
+    kernels run on: from another stream's pool they could be memory that this
+    one's pending work still uses, and a workspace would go back there while
+    the kernels run."""
+    if stream is None:
+        return _HERE
+    import torch
+    return torch.cuda.stream(stream)
+
+
+def _int32(**sizes):
+    """The C calls take sizes as int: refused here, since ctypes would cut them."""
+    for name, value in sizes.items():
+        if not -0x80000000 <= value <= 0x7fffffff:
+            raise ValueError(f"{name}: {value} is not in [-2^31, 2^31)")
+
+
 # ---------------------------------------------------------------- gated linear recurrence
 
 
@@ -455,14 +476,18 @@ def _recurrence_sizes(log_alpha, cu_seqlens):
     if cu_seqlens is None:
         if log_alpha.dim() != 3:
             raise ValueError(f"log_alpha: expected [B,T,D], got {tuple(log_alpha.shape)}")
-        return tuple(log_alpha.shape)
+        N, T, D = log_alpha.shape
+        _int32(B=N, T=T, D=D)
+        return N, T, D
     if log_alpha.dim() != 2:
         raise ValueError(f"log_alpha: expected packed [total_T,D], got {tuple(log_alpha.shape)}")
     N = cu_seqlens.numel() - 1
     if N < 0:
         raise ValueError("cu_seqlens: expected N + 1 offsets")
+    T, D = log_alpha.shape
+    _int32(N=N, total_T=T, D=D)
     _need(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32, log_alpha.device)
-    return N, log_alpha.shape[0], log_alpha.shape[1]
+    return N, T, D
 
 
 def recurrence_fwd(log_alpha, x, h0=None, *, cu_seqlens=None, output_final_state: bool = True, h=None, h_T=None,
@@ -482,14 +507,15 @@ def recurrence_fwd(log_alpha, x, h0=None, *, cu_seqlens=None, output_final_state
     _need(x, "x", shape, dt, dev)
     if h0 is not None:
         _need(h0, "h0", (N, D), torch.float32, dev)
-    if h is None:
-        h = torch.empty_like(x)
-    else:
+    if h is not None:
         _need(h, "h", shape, dt, dev)
     if h_T is not None:
         _need(h_T, "h_T", (N, D), torch.float32, dev)
-    elif output_final_state:
-        h_T = torch.empty(N, D, dtype=torch.float32, device=dev)
+    with _memory_of(stream):
+        if h is None:
+            h = torch.empty_like(x)
+        if h_T is None and output_final_state:
+            h_T = torch.empty(N, D, dtype=torch.float32, device=dev)
     with _on(dev):
         code = lib.kda_recurrence_fwd(_ptr(log_alpha), _ptr(x), _ptr(h0), _ptr(h), _ptr(h_T), _ptr(cu_seqlens),
                                       N, T, D, _DTYPE[dts], _stream(stream, dev))
@@ -514,8 +540,9 @@ def recurrence_bwd(log_alpha, h, h0, dh, dh_T=None, *, cu_seqlens=None, want_dh0
         _need(h0, "h0", (N, D), torch.float32, dev)
     if dh_T is not None:
         _need(dh_T, "dh_T", (N, D), torch.float32, dev)
-    g = {"dx": torch.empty_like(dh), "dlog_alpha": torch.empty_like(log_alpha),
-         "dh0": torch.empty(N, D, dtype=torch.float32, device=dev) if want_dh0 else None}
+    with _memory_of(stream):
+        g = {"dx": torch.empty_like(dh), "dlog_alpha": torch.empty_like(log_alpha),
+             "dh0": torch.empty(N, D, dtype=torch.float32, device=dev) if want_dh0 else None}
     with _on(dev):
         code = lib.kda_recurrence_bwd(_ptr(log_alpha), _ptr(h), _ptr(h0), _ptr(dh), _ptr(dh_T), _ptr(g["dx"]),
                                       _ptr(g["dlog_alpha"]), _ptr(g["dh0"]), _ptr(cu_seqlens), N, T, D, _DTYPE[dts],
@@ -533,6 +560,7 @@ def recurrence_step(log_alpha, x, h, *, h_out=None, y=None, stream=None):
     if log_alpha.dim() != 2:
         raise ValueError(f"log_alpha: expected [N,D], got {tuple(log_alpha.shape)}")
     N, D = log_alpha.shape
+    _int32(N=N, D=D)
     dt, dev = log_alpha.dtype, log_alpha.device
     dts = _dtype_of(log_alpha)
     _need(log_alpha, "log_alpha", (N, D), dt, dev)
@@ -543,7 +571,8 @@ def recurrence_step(log_alpha, x, h, *, h_out=None, y=None, stream=None):
     else:
         _need(h_out, "h_out", (N, D), torch.float32, dev)
     if y is None:
-        y = torch.empty_like(x)
+        with _memory_of(stream):
+            y = torch.empty_like(x)
     else:
         _need(y, "y", (N, D), dt, dev)
     with _on(dev):
@@ -618,6 +647,7 @@ def _qk_args(q, k, q_weight, k_weight, cos, sin, positions, norm):
         q, k = _heads_view(q, "q", qs[:-2], d, dt, dev), _heads_view(k, "k", qs[:-2], d, dt, dev)
         sq, sk = q.stride(), k.stride()
     n = q.shape[0]
+    _int32(tokens=n)
     if q_weight is not None:
         _need(q_weight, "q_weight", (d,), dt, dev)
     if k_weight is not None:
@@ -661,14 +691,15 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positio
     dts = _dtype_of(q)
     inputs, sizes = _qk_args(q, k, q_weight, k_weight, cos, sin, positions, norm)
     dt, dev = q.dtype, q.device
-    if q_out is None:
-        q_out = torch.empty(q.shape, dtype=dt, device=dev)
-    else:
+    if q_out is not None:
         _need(q_out, "q_out", q.shape, dt, dev)
-    if k_out is None:
-        k_out = torch.empty(k.shape, dtype=dt, device=dev)
-    else:
+    if k_out is not None:
         _need(k_out, "k_out", k.shape, dt, dev)
+    with _memory_of(stream):
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=dt, device=dev)
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=dt, device=dev)
     with _on(dev):
         code = lib.kda_qk_norm_rope(*inputs, q_out.data_ptr(), k_out.data_ptr(), *sizes, eps, q_scale,
                                     1 if interleaved else 0, _DTYPE[dts], _stream(stream, dev))
@@ -695,11 +726,12 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, cos=Non
     dt, dev, d = q.dtype, q.device, q.shape[-1]
     _need(dq_out, "dq_out", q.shape, dt, dev)
     _need(dk_out, "dk_out", k.shape, dt, dev)
-    dq, dk = torch.empty(q.shape, dtype=dt, device=dev), torch.empty(k.shape, dtype=dt, device=dev)
-    dqw = None if q_weight is None else torch.empty(d, dtype=torch.float32, device=dev)
-    dkw = None if k_weight is None else torch.empty(d, dtype=torch.float32, device=dev)
-    if workspace is None and (dqw is not None or dkw is not None):
-        workspace = torch.empty(_qk_workspace_size(*sizes[:4]), dtype=torch.uint8, device=dev)
+    with _memory_of(stream):
+        dq, dk = torch.empty(q.shape, dtype=dt, device=dev), torch.empty(k.shape, dtype=dt, device=dev)
+        dqw = None if q_weight is None else torch.empty(d, dtype=torch.float32, device=dev)
+        dkw = None if k_weight is None else torch.empty(d, dtype=torch.float32, device=dev)
+        if workspace is None and (dqw is not None or dkw is not None):
+            workspace = torch.empty(_qk_workspace_size(*sizes[:4]), dtype=torch.uint8, device=dev)
     ws_len = 0 if workspace is None else workspace.numel() * workspace.element_size()
     with _on(dev):
         code = lib.kda_qk_norm_rope_bwd(dq_out.data_ptr(), dk_out.data_ptr(), *inputs, dq.data_ptr(), dk.data_ptr(),
@@ -736,6 +768,8 @@ def attn_decode(q, k_cache, v_cache, page_table, seq_lens, *, k=None, v=None, sc
     N, Hq, d = q.shape
     n_pages, Hk, page_size, _ = k_cache.shape
     max_pages = page_table.shape[1]
+    window = int(window)
+    _int32(N=N, Hq=Hq, n_pages=n_pages, Hk=Hk, page_size=page_size, max_pages=max_pages, window=window)
     dt, dev = q.dtype, q.device
     dts = _dtype_of(q)
     _need(q, "q", (N, Hq, d), dt, dev)
@@ -748,23 +782,24 @@ def attn_decode(q, k_cache, v_cache, page_table, seq_lens, *, k=None, v=None, sc
     if k is not None:
         _need(k, "k", (N, Hk, d), dt, dev)
         _need(v, "v", (N, Hk, d), dt, dev)
-    if o is None:
-        o = torch.empty_like(q)
-    else:
+    if o is not None:
         _need(o, "o", (N, Hq, d), dt, dev)
     if lse is not None:
         _need(lse, "lse", (N, Hq), torch.float32, dev)
         return_lse = True
-    elif return_lse:
-        lse = torch.empty(N, Hq, dtype=torch.float32, device=dev)
     ws_bytes = attn_decode_workspace_size(N, Hq, Hk, d)
-    if ws_bytes and workspace is None:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    with _memory_of(stream):
+        if o is None:
+            o = torch.empty_like(q)
+        if lse is None and return_lse:
+            lse = torch.empty(N, Hq, dtype=torch.float32, device=dev)
+        if ws_bytes and workspace is None:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
     ws_len = 0 if workspace is None else workspace.numel() * workspace.element_size()
     with _on(dev):
         code = lib.kda_attn_decode(_ptr(q), _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(page_table),
                                    _ptr(seq_lens), _ptr(o), _ptr(lse), N, Hq, Hk, d, n_pages, page_size, max_pages,
-                                   int(window), d ** -0.5 if scale is None else scale, _DTYPE[dts], _ptr(workspace),
+                                   window, d ** -0.5 if scale is None else scale, _DTYPE[dts], _ptr(workspace),
                                    ws_len, _stream(stream, dev))
     _check("kda_attn_decode", code)
     return (o, lse) if return_lse else o

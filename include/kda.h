@@ -359,8 +359,8 @@ kda_status_t kda_noalloc_status(void *stream);
  *   T >= 0, D in [1, 2^30] (any width; rows of 16-byte multiples are the fast
  *   case).
  * An empty sequence copies h0 to h_T. State and sums in fp32; decays over
- * spans of tokens are exponentials of fp32 sums of log_alpha. Nothing depends
- * on timing: equal inputs give equal bits.
+ * spans of tokens are fp32 products of the tokens' decays, in an order that the
+ * sizes alone decide. Nothing depends on timing: equal inputs give equal bits.
  */
 kda_status_t kda_recurrence_fwd(const void *log_alpha, const void *x, const float *h0, void *h, float *h_T,
                                 const int *cu_seqlens, int N, int T, int D, kda_dtype_t dtype, void *stream);

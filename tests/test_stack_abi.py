@@ -130,3 +130,16 @@ def test_binding_refuses_cpu_tensors():
     q, cache = torch.zeros(2, 4, 64), torch.zeros(3, 2, 16, 64)
     with pytest.raises(ValueError, match="CUDA tensor"):
         kda.attn_decode(q, cache, cache, torch.zeros(2, 2, dtype=torch.int32), torch.zeros(2, dtype=torch.int32))
+
+
+def test_binding_refuses_sizes_past_int32():
+    far = torch.empty(2 ** 32 + 5, 1, device="meta")
+    cu = torch.zeros(2, dtype=torch.int32)
+    for call in (lambda: kda.recurrence_fwd(far, far, cu_seqlens=cu), lambda: kda.recurrence_fwd(far[None], far[None]),
+                 lambda: kda.recurrence_step(far, far, far)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            call()
+    q, cache = torch.zeros(1, 1, 64), torch.zeros(1, 1, 16, 64)
+    for window in (2 ** 32 + 5, -2 ** 32):
+        with pytest.raises(ValueError, match="window"):
+            kda.attn_decode(q, cache, cache, torch.zeros(1, 1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32), window=window)
