@@ -167,19 +167,18 @@ __device__ __forceinline__ void copy_tile(unsigned char* slot, const T* first, i
             cp_async16(slot + (i * THREADS + threadIdx.x) * 16, first + (long long)(k0 + i) * step + c, k0 + i < left && c < D);
     } else {
         const int bytes = min(D - c0, (int)(128 / sizeof(T))) * (int)sizeof(T);
-        const char* base = reinterpret_cast<const char*>(first + (long long)warp * 4 * R * step + c0);
-        left -= warp * 4 * R;
-        unsigned char* to = slot + warp * 4 * group_bytes<ALIGN, R>();
+        auto copy = [&](int k, int piece) {  // k: token of the CTA's tile
+            const uintptr_t row = reinterpret_cast<uintptr_t>(first + (long long)k * step + c0);
+            const uintptr_t from = (row & ~(uintptr_t)15) + piece * 16;
+            int n = k < left && piece * 16 < (int)(row & 15) + bytes ? 16 : 0;
+            if (n && from + 16 > reinterpret_cast<uintptr_t>(stop)) n = (int)(reinterpret_cast<uintptr_t>(stop) - from);
+            cp_async16_some(slot + (k / R) * group_bytes<ALIGN, R>() + (k % R * kRowPieces + piece) * 16, reinterpret_cast<const void*>(from), n);
+        };
+        // a token group's eight lanes take the first eight pieces of its rows, then the warp's lanes a ninth piece each
 #pragma unroll
-        for (int j = 0; j < (4 * R * kRowPieces + 31) / 32; ++j) {
-            const int q = j * 32 + lane, k = q / kRowPieces, piece = q % kRowPieces;
-            if (4 * R * kRowPieces % 32 != 0 && k >= 4 * R) continue;
-            const uintptr_t row = reinterpret_cast<uintptr_t>(base + (long long)k * step * (int)sizeof(T));
-            const char* from = reinterpret_cast<const char*>(row & ~(uintptr_t)15) + piece * 16;
-            const bool on = k < left && piece * 16 < (int)(row & 15) + bytes;
-            const long long there = reinterpret_cast<const char*>(stop) - from;
-            cp_async16_some(to + (k / R) * group_bytes<ALIGN, R>() + (k % R * kRowPieces + piece) * 16, from, on ? (int)min(there, 16ll) : 0);
-        }
+        for (int i = 0; i < R; ++i) copy((threadIdx.x >> 3) * R + i, lane & 7);
+        static_assert(4 * R <= 32);
+        if (lane < 4 * R) copy(warp * 4 * R + lane, 8);
     }
 }
 // This thread's channels of its token i; `off`: the row's first byte modulo 16.
