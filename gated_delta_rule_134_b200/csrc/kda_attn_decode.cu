@@ -374,7 +374,8 @@ __device__ __forceinline__ bool find_range(const AttnDecodeArgs& a, const Pieces
 // are split into two tf32 parts each, and three products taken (the fourth,
 // lo * lo, is below 2^-22 of the whole), which keeps 32-bit accuracy. The split
 // is integer rounding and a subtraction: with the conversion instruction in its
-// place 64 rows of 1000 positions took 169 us, now 95.
+// place 64 rows of 1000 positions took 169 us, with these 95 (and 99 since every
+// tile's products are added outside the MMA).
 // The weights' maximum is a reference that moves only when a score passes it by
 // more than 2^8: until then weights reach 2^8, far from any overflow in 32
 // bits, and neither a reduction over the warp nor a rescaling is due.
@@ -554,7 +555,10 @@ __global__ void __launch_bounds__(Plan<T, D>::kWarps * 32, Plan<T, D>::kCtasPerS
             const uint32_t v0 = vt + c2 * RB + (((g >> 2) ^ c2) << 4) + (g & 3) * 4;              // channel g of position 2 c
             const uint32_t v1 = vt + (c2 + 1) * RB + (((g >> 2) ^ (c2 + 1)) << 4) + (g & 3) * 4;  // of 2 c + 1
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i)
+            for (int i = 0; i < D / 16; ++i) {
+                // A tile's products by themselves, then added here: the MMA rounds its sums towards zero, which over a
+                // hundred tiles would be off by 2^-16.
+                float add[NT][4] = {};
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
                     uint32_t hi[4], lo[4];
@@ -563,11 +567,16 @@ __global__ void __launch_bounds__(Plan<T, D>::kWarps * 32, Plan<T, D>::kCtasPerS
                         split_tf32(lds_f32(((e >> 1 ? v1 : v0) ^ ((i & 1) * 64 + (e & 1) * 32)) + b * 8 * RB + (i >> 1) * 128), hi[e], lo[e]);
 #pragma unroll
                     for (int j = 0; j < NT; ++j) {
-                        mma_tf32(o[i][j], lo, ph[b][j][0], ph[b][j][1]);
-                        mma_tf32(o[i][j], hi, pl[b][j][0], pl[b][j][1]);
-                        mma_tf32(o[i][j], hi, ph[b][j][0], ph[b][j][1]);
+                        mma_tf32(add[j], lo, ph[b][j][0], ph[b][j][1]);
+                        mma_tf32(add[j], hi, pl[b][j][0], pl[b][j][1]);
+                        mma_tf32(add[j], hi, ph[b][j][0], ph[b][j][1]);
                     }
                 }
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[i][j][e] += add[j][e];
+            }
         }
         if (bits & kEnds) {
             const int place = (int)(bits >> kPlaceShift);

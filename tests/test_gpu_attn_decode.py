@@ -289,3 +289,21 @@ def test_refusals(cuda_lib):
         cuda_lib.attn_decode(s["q"], s["kc"], s["vc"], s["table"], s["lens"], scale=math.nan)
     with pytest.raises(TypeError):
         cuda_lib.attn_decode(s["q"].half(), s["kc"].half(), s["vc"].half(), s["table"], s["lens"])
+
+
+@pytest.mark.parametrize("d,Hq", [(64, 4), (128, 4), (64, 64), (128, 64)])
+def test_long_sums_are_rounded_to_nearest(cuda_lib, d, Hq):
+    """All values 1: o is the sum of the weights over itself, so a sum that is rounded towards zero shows as o < 1. A warp
+    adds W tiles of 16 positions: W roundings in the numerator and 2 W in the denominator, some twenty where pieces are
+    joined. Rounded to nearest they are independent, each 2^-24 at most: 6 2^-24 sqrt(3 W + 20). Within a tile the products
+    may be summed as the MMA likes, six steps of 2^-23, and a weight's second tf32 part is cut 2^-22 below it."""
+    N, Hk, page, L = 256, 4, 64, 4096
+    g = torch.Generator("cuda").manual_seed(41)
+    kc = torch.randn(L // page, Hk, page, d, device="cuda", generator=g)
+    vc = torch.ones_like(kc)
+    table = torch.arange(L // page, dtype=torch.int32, device="cuda").repeat(N, 1)  # every row reads the same pages
+    lens = torch.full((N,), L, dtype=torch.int32, device="cuda")
+    q = torch.randn(N, Hq, d, device="cuda", generator=g)
+    o = cuda_lib.attn_decode(q, kc, vc, table, lens)
+    W = N * Hk * (L // 16) / 1036  # 1036: the fewest warps that share the work
+    assert float((o.double() - 1).abs().max()) <= 6 * 2 ** -24 * math.sqrt(3 * W + 20) + 8 * 2 ** -23
