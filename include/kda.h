@@ -502,6 +502,9 @@ kda_status_t kda_qk_norm_rope_bwd(const void *d_q_out, const void *d_k_out, cons
  * any attended position gives o = 0 and lse = -INFINITY. Rows of a page behind
  * its sequence's last position are never read into a sum (they may hold NaN).
  * The page that takes a new token must belong to its sequence alone.
+ * The sums over positions are divided by the weights' sum at the end only, and
+ * a weight reaches 2^8: |v| times 2^8 times the number of positions has to stay
+ * finite in fp32, and so have the scores (else o holds infinities or NaN).
  * Scores, softmax statistics and sums in fp32; with KDA_BF16 the softmax
  * weights are rounded to bf16 for the product with V. Equal inputs give equal
  * bits.
