@@ -692,7 +692,9 @@ __global__ void __launch_bounds__((WARPS == 1 ? kJoinWarps : WARPS) * 32) attn_j
         for (int e = 0; e < E; ++e) acc[e] *= keep;
 #pragma unroll
         for (int b = 0; b < B; ++b) {
-            if (ml[b].x == -INFINITY) continue;  // nothing attended in this piece
+            // Nothing attended in this piece, or no such piece. The maximum would not tell: it passes over NaN scores, and
+            // stays -inf where a piece has no others. Their sum is NaN, and goes on.
+            if (ml[b].y == 0.f) continue;
             const float f = exp2_fast(ml[b].x - top);
             sum = fmaf(ml[b].y, f, sum);
 #pragma unroll
@@ -712,7 +714,7 @@ __global__ void __launch_bounds__((WARPS == 1 ? kJoinWarps : WARPS) * 32) attn_j
         sum = 0.f;
 #pragma unroll
         for (int w = 0; w < WARPS; ++w) ref = fmaxf(ref, sml[w].x);
-        auto factor = [&](int w) { return sml[w].x == -INFINITY ? 0.f : exp2_fast(sml[w].x - ref); };
+        auto factor = [&](int w) { return sml[w].y == 0.f ? 0.f : exp2_fast(sml[w].x - ref); };
 #pragma unroll
         for (int w = 0; w < WARPS; ++w) sum = fmaf(sml[w].y, factor(w), sum);
         for (int c = threadIdx.x; c < D; c += WARPS * 32) {

@@ -307,3 +307,29 @@ def test_long_sums_are_rounded_to_nearest(cuda_lib, d, Hq):
     o = cuda_lib.attn_decode(q, kc, vc, table, lens)
     W = N * Hk * (L // 16) / 1036  # 1036: the fewest warps that share the work
     assert float((o.double() - 1).abs().max()) <= 6 * 2 ** -24 * math.sqrt(3 * W + 20) + 8 * 2 ** -23
+
+
+# Which warps hold a pair: (lengths, Hq, Hk, page). The work is cut into equal ranges for the 1000 to 2000 warps of a call,
+# so a few long rows are split (32 warps join the pieces of fewer than 16 pairs, 8 those of fewer than 148, one the others)
+# and among many short ones some pairs are whole.
+SPLITS = {"32 warps join": ([20000], 2, 1, 256), "8 warps join": ([2000] * 16, 4, 2, 256), "a warp joins": ([300] * 40, 8, 4, 100),
+          "whole pairs": ([60] * 256, 16, 8, 16), "17 heads": ([20000], 17, 1, 256)}
+
+
+@pytest.mark.parametrize("what", ["q", "k", "v"])
+@pytest.mark.parametrize("split", list(SPLITS))
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_attended_nan_comes_out(cuda_lib, dtype, split, what):
+    """A NaN query, or a page of NaN keys or values, longer than a piece, makes its heads NaN, whichever warps hold them."""
+    lens, Hq, Hk, page = SPLITS[split]
+    s = make(lens, Hq, Hk, 64, page, dtype, 51)
+    if what == "q":
+        s["q"][len(lens) // 2, Hq - 1] = math.nan
+    else:
+        pages = s["table"][len(lens) // 2]
+        s[what + "c"][int(pages[min(1, len(pages) - 1)]), Hk - 1, : min(page, lens[0] // 2)] = math.nan
+    o, lse = check(cuda_lib, s)
+    bad, G = torch.zeros(len(lens), Hq, dtype=torch.bool), Hq // Hk
+    bad[len(lens) // 2, Hq - 1 if what == "q" else Hq - G:] = True
+    assert torch.equal(o.isnan().any(-1).cpu(), bad) and torch.equal(o.isnan().all(-1).cpu(), bad)
+    assert torch.equal(lse.isnan().cpu(), bad if what != "v" else torch.zeros_like(bad))
