@@ -118,6 +118,13 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// Two weights as two bf16 parts each, hi and lo = x - hi rounded, together off by 2^-16 x at most. hi is x cut to bf16 from
+// just below, so that lo is above 0 too (in bf16, for x above 2^-110): an infinite value keeps its sign.
+__device__ __forceinline__ void split_bf16(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+    const uint32_t h0 = __float_as_uint(x0 * (1.f - 0x1p-23f)), h1 = __float_as_uint(x1 * (1.f - 0x1p-23f));
+    hi = __byte_perm(h0, h1, 0x7632);
+    lo = pack_bf16(x0 - __uint_as_float(h0 & 0xffff0000u), x1 - __uint_as_float(h1 & 0xffff0000u));
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t y;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -370,8 +377,12 @@ __device__ __forceinline__ bool find_range(const AttnDecodeArgs& a, const Pieces
 // The positions are the rows of the MMAs, the query heads their columns (NT
 // blocks of 8), so that few heads waste little:
 //     S^T [16 x 8 NT] = K Q^T,  O^T [D x 8 NT] += V^T P^T.
-// bf16 operands go in as they are, the weights rounded to bf16. 32-bit operands
-// are split into two tf32 parts each, and three products taken (the fourth,
+// bf16 operands go in as they are, the weights in two parts of bf16 with a
+// product each: one part alone, 2^-9 off a weight, costs as much accuracy again
+// as the rounding of the output, and saves little (64 rows of 256 to 16384
+// positions 170.7 us, with both 171.7; 256 rows of 0 to 300 21.8 and 22.5; 32
+// heads to a key-value head of 64, 64 rows of 2048, 31.5 and 34.3). 32-bit
+// operands are split into two tf32 parts each, and three products taken (the fourth,
 // lo * lo, is below 2^-22 of the whole), which keeps 32-bit accuracy. The split
 // is integer rounding and a subtraction: with the conversion instruction in its
 // place 64 rows of 1000 positions took 169 us, with these 95 (and 99 since every
@@ -524,18 +535,25 @@ __global__ void __launch_bounds__(Plan<T, D>::kWarps * 32, Plan<T, D>::kCtasPerS
                 l[j][e] += s[j][e] + s[j][e + 2];
             }
         if constexpr (BF) {
-            uint32_t pf[NT][2];  // the weights as the right operand (at most half a step off each; l sums them unrounded)
+            uint32_t ph[NT][2], pl[NT][2];  // the weights' two parts as the right operand
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                pf[j][0] = transpose8x8(pack_bf16(s[j][0], s[j][1]));
-                pf[j][1] = transpose8x8(pack_bf16(s[j][2], s[j][3]));
-            }
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    uint32_t hi, lo;
+                    split_bf16(s[j][2 * b], s[j][2 * b + 1], hi, lo);
+                    ph[j][b] = transpose8x8(hi);
+                    pl[j][b] = transpose8x8(lo);
+                }
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
                 uint32_t vf[4];
                 ldsm4_trans(vf, vt + v_at + (((2 * i + (mat & 1)) ^ r8) << 4));
 #pragma unroll
-                for (int j = 0; j < NT; ++j) mma_bf16(o[i][j], vf, pf[j][0], pf[j][1]);
+                for (int j = 0; j < NT; ++j) {
+                    mma_bf16(o[i][j], vf, pl[j][0], pl[j][1]);
+                    mma_bf16(o[i][j], vf, ph[j][0], ph[j][1]);
+                }
             }
         } else {
             // Inner index x of the right operand stands for position 2 x (x < 4) or 2 (x - 4) + 1 of 8: lane 4 h + c holds

@@ -506,8 +506,7 @@ kda_status_t kda_qk_norm_rope_bwd(const void *d_q_out, const void *d_k_out, cons
  * a weight reaches 2^8: |v| times 2^8 times the number of positions has to stay
  * finite in fp32, and so have the scores (else o holds infinities or NaN).
  * Scores, softmax statistics and sums in fp32; with KDA_BF16 the softmax
- * weights are rounded to bf16 for the product with V. Equal inputs give equal
- * bits.
+ * weights go into the product with V to 16 bits. Equal inputs give equal bits.
  */
 size_t kda_attn_decode_workspace_size(int N, int Hq, int Hk, int d);
 kda_status_t kda_attn_decode(const void *q, const void *k_new, const void *v_new, void *k_cache, void *v_cache,

@@ -333,3 +333,19 @@ def test_attended_nan_comes_out(cuda_lib, dtype, split, what):
     bad[len(lens) // 2, Hq - 1 if what == "q" else Hq - G:] = True
     assert torch.equal(o.isnan().any(-1).cpu(), bad) and torch.equal(o.isnan().all(-1).cpu(), bad)
     assert torch.equal(lse.isnan().cpu(), bad if what != "v" else torch.zeros_like(bad))
+
+
+@pytest.mark.parametrize("Hq,Hk", [(4, 2), (16, 1), (20, 1)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_bf16_caches_keep_the_weights(cuda_lib, d, Hq, Hk):
+    """On bf16 caches only the output is rounded to bf16. The bound is that of 32-bit weights, and beside it what two bf16
+    parts leave of a weight (2^-8 of 2^-8 of it) and what the MMA cuts from its sums: for each tile two products of four
+    steps, 2^-23 of the weighted magnitudes each."""
+    s = make([1, 2, 3, 17, 40, 700], Hq, Hk, d, 16, "bf16", 61)
+    c = {n: t.cuda() for n, t in s.items()}
+    o = cuda_lib.attn_decode(c["q"], c["kc"], c["vc"], c["table"], c["lens"], k=c["k"], v=c["v"])
+    f = {n: t.float() if t.is_floating_point() else t for n, t in s.items()}
+    (want, slack), _ = R.attn_decode(f["q"], f["kc"], f["vc"], f["table"], f["lens"], f["k"], f["v"])
+    (size, _), _ = R.attn_decode(f["q"], f["kc"], f["vc"].abs(), f["table"], f["lens"], f["k"], f["v"].abs())
+    tiles = (s["lens"].double()[:, None, None] + 16) // 16
+    R.close(o, want, slack + (2.0 ** -16 + 8 * tiles * 2.0 ** -23) * size)
