@@ -115,7 +115,8 @@ template <int LANES> __device__ __forceinline__ F2 group_sum2(F2 x) {
 }
 
 // r of a head from its sum of squares. Where that leaves 32 bits the head is
-// rescaled by 2^-80 first (eps is then far below the sum).
+// rescaled by 2^-80 first, and eps by 2^-160 (a large one still counts beside it).
+__device__ __forceinline__ float small_eps(float eps) { return eps * 0x1p-80f * 0x1p-80f; }
 template <typename T, int LANES>
 __device__ __forceinline__ float rnorm(const Raw<T>& x, float ss, float share, float eps) {
     float r = rsqrtf(fmaf(ss, share, eps));
@@ -125,7 +126,7 @@ __device__ __forceinline__ float rnorm(const Raw<T>& x, float ss, float share, f
 #pragma unroll
         for (int e = 0; e < 8; ++e) s = fmaf(x.get(e) * 0x1p-80f, x.get(e) * 0x1p-80f, s);
         s = group_sum<LANES>(s);
-        if (out) r = 0x1p-80f * rsqrtf(s * share);
+        if (out) r = 0x1p-80f * rsqrtf(fmaf(s, share, small_eps(eps)));
     }
     return r;
 }
@@ -388,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 2) qk_bwd_kernel(QkArgs a, int q_chu
                 if (out) {
                     ux = small;
                     all.y = again.y;
-                    r = rsqrtf(again.x * share);
+                    r = rsqrtf(fmaf(again.x, share, small_eps(a.eps)));
                     r_out = 0x1p-80f * r;
                 }
             }

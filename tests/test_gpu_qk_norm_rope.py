@@ -246,3 +246,15 @@ def test_refusals(cuda_lib):
         cuda_lib.qk_norm_rope_bwd(s["dq"][:3], s["dk"], q, k)
     with pytest.raises(cuda_lib.KDAError, match="workspace"):
         cuda_lib.qk_norm_rope_bwd(s["dq"], s["dk"], q, k, s["wq"], workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("norm", ["rms", "l2"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_large_eps(cuda_lib, dtype, norm):
+    """An eps beside which heads whose squares leave 32 bits are small, like, and large."""
+    s = make(12, 2, 2, 64, 64, dtype, 32, fused=False)
+    for t, f in ((1, 1e15), (2, 1e18), (3, 1e19), (4, 1e20), (5, 1e25)):
+        s["q"][t] *= f
+        s["k"][t] *= f
+    for eps in (1e30, 1e37, 2.5e38):
+        check(cuda_lib, s, norm, eps=eps)
