@@ -258,3 +258,16 @@ def test_large_eps(cuda_lib, dtype, norm):
         s["k"][t] *= f
     for eps in (1e30, 1e37, 2.5e38):
         check(cuda_lib, s, norm, eps=eps)
+
+
+@pytest.mark.parametrize("norm", ["rms", "l2"])
+@pytest.mark.parametrize("d,rot", [(8, 0), (64, 64), (128, 64), (256, 256)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_gradients_of_huge_heads(cuda_lib, dtype, d, rot, norm):
+    """Heads whose squares leave 32 bits, beside ordinary ones of the same warp; their gradients do not (1e-18 to 1e-36)."""
+    s = make(40, 4, 2, d, rot, dtype, 31, fused=False)
+    for t, f in ((1, 1e18), (2, 3e19), (7, 1e30), (8, 1e36)):
+        s["q"][t, 1] *= f
+        s["k"][t + 2] *= f
+    check(cuda_lib, s, norm)
+    check(cuda_lib, s, norm, interleaved=True, scale=0.125)
