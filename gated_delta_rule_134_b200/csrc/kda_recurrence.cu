@@ -71,7 +71,10 @@ template <typename T> struct Pack {
     }
 };
 
-// e^x. For bf16 inputs 2^(x log2 e), off by 2^-22 for |x| < 1: far below the input's own step.
+// e^x. For bf16 inputs 2^(x log2 e) by one instruction. All of them tried, it is as near as expf for |x| < 1 (both 1.9 times
+// 2^-24 off at most, 1.4 for |x| < 2^-8: slow decays over long sequences lose nothing); beyond that the roundings of log2 e
+// and of the product count, at most 2 |x| 2^-24 of a decay that is small then. With expf the forward pass of B4 T8192 D4096
+// takes 148 us, so 134.
 template <typename T> __device__ __forceinline__ float decay(float x);
 template <> __device__ __forceinline__ float decay<float>(float x) { return expf(x); }
 template <> __device__ __forceinline__ float decay<__nv_bfloat16>(float x) {

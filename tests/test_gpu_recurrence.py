@@ -327,3 +327,22 @@ def test_refusals(cuda_lib):
     odd = torch.zeros(2 * 8 * 16 + 1, device="cuda")[1:].view(2, 8, 16)
     with pytest.raises(cuda_lib.KDAError, match="misaligned"):
         cuda_lib.recurrence_fwd(odd, la)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_decays(cuda_lib, dtype):
+    """h = exp(log_alpha) from a state of 1 shows the decays of the scan, its backward pass and the step, at all bf16 values
+    from -2^-24 to -87. expf is off by 2 U = 2^-23 at most. The scans' 2^(x log2 e) of bf16 inputs: 4 U by the instruction;
+    log2 e and the product are rounded by U each, of an exponent y = |x| log2 e, and 2^y is off by ln 2 y of that: 2 |x| U."""
+    bits = torch.arange(0xB380, 0xC2AE + 1, dtype=torch.int32).to(torch.int16)
+    la = bits.view(torch.bfloat16).to(DT[dtype])[None, None]
+    D = la.shape[-1]
+    one, zero = torch.ones(1, D, device="cuda"), torch.zeros(1, 1, D, dtype=DT[dtype], device="cuda")
+    h, end = cuda_lib.recurrence_fwd(la.cuda(), zero, one)
+    grads = cuda_lib.recurrence_bwd(la.cuda(), h, one, zero, one)
+    _, step = cuda_lib.recurrence_step(la[0].cuda(), zero[0], one, h_out=torch.empty_like(one))
+    x = la[0].double()
+    scan = 2 * R.U if dtype == "f32" else (4 + 2 * x.abs()) * R.U
+    for got, bound, what in ((end, scan, "scan"), (grads["dh0"], scan, "backward"), (step, 2 * R.U, "step")):
+        off = (got.cpu().double() / x.exp() - 1).abs()
+        assert bool((off <= bound).all()), (what, float((off / R.U).max()))
