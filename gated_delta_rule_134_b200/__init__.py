@@ -460,6 +460,17 @@ def _memory_of(stream):
     return torch.cuda.stream(stream)
 
 
+def _scratch_bytes(workspace, device) -> int:
+    """Size of a workspace that the caller gave (or None): the kernels write all of it, so its elements have to be memory
+    of its own, on the tensors' device."""
+    if workspace is None:
+        return 0
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace: expected a contiguous tensor on {device}, got strides {tuple(workspace.stride())} of "
+                         f"{tuple(workspace.shape)} on {workspace.device}")
+    return workspace.numel() * workspace.element_size()
+
+
 def _int32(**sizes):
     """The C calls take sizes as int: refused here, since ctypes would cut them."""
     for name, value in sizes.items():
@@ -726,13 +737,14 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, cos=Non
     dt, dev, d = q.dtype, q.device, q.shape[-1]
     _need(dq_out, "dq_out", q.shape, dt, dev)
     _need(dk_out, "dk_out", k.shape, dt, dev)
+    ws_len = _scratch_bytes(workspace, dev)
     with _memory_of(stream):
         dq, dk = torch.empty(q.shape, dtype=dt, device=dev), torch.empty(k.shape, dtype=dt, device=dev)
         dqw = None if q_weight is None else torch.empty(d, dtype=torch.float32, device=dev)
         dkw = None if k_weight is None else torch.empty(d, dtype=torch.float32, device=dev)
         if workspace is None and (dqw is not None or dkw is not None):
-            workspace = torch.empty(_qk_workspace_size(*sizes[:4]), dtype=torch.uint8, device=dev)
-    ws_len = 0 if workspace is None else workspace.numel() * workspace.element_size()
+            ws_len = _qk_workspace_size(*sizes[:4])
+            workspace = torch.empty(ws_len, dtype=torch.uint8, device=dev)
     with _on(dev):
         code = lib.kda_qk_norm_rope_bwd(dq_out.data_ptr(), dk_out.data_ptr(), *inputs, dq.data_ptr(), dk.data_ptr(),
                                         _ptr(dqw), _ptr(dkw), *sizes, eps, q_scale, 1 if interleaved else 0,
@@ -787,15 +799,15 @@ def attn_decode(q, k_cache, v_cache, page_table, seq_lens, *, k=None, v=None, sc
     if lse is not None:
         _need(lse, "lse", (N, Hq), torch.float32, dev)
         return_lse = True
-    ws_bytes = attn_decode_workspace_size(N, Hq, Hk, d)
+    ws_len = _scratch_bytes(workspace, dev)
     with _memory_of(stream):
         if o is None:
             o = torch.empty_like(q)
         if lse is None and return_lse:
             lse = torch.empty(N, Hq, dtype=torch.float32, device=dev)
-        if ws_bytes and workspace is None:
-            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
-    ws_len = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        if workspace is None:
+            ws_len = attn_decode_workspace_size(N, Hq, Hk, d)
+            workspace = torch.empty(ws_len, dtype=torch.uint8, device=dev) if ws_len else None
     with _on(dev):
         code = lib.kda_attn_decode(_ptr(q), _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(page_table),
                                    _ptr(seq_lens), _ptr(o), _ptr(lse), N, Hq, Hk, d, n_pages, page_size, max_pages,

@@ -143,3 +143,22 @@ def test_binding_refuses_sizes_past_int32():
     for window in (2 ** 32 + 5, -2 ** 32):
         with pytest.raises(ValueError, match="window"):
             kda.attn_decode(q, cache, cache, torch.zeros(1, 1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32), window=window)
+
+
+@pytest.mark.parametrize("bad", ["other device", "expanded", "strided"])
+def test_binding_refuses_workspaces_that_are_not_its_memory(bad):
+    """Tensors that stand for CUDA tensors without memory: a call that went on would fail in another way."""
+    from torch._subclasses import FakeTensorMode
+    with FakeTensorMode():
+        cuda = dict(device="cuda", dtype=torch.bfloat16)
+        i32 = dict(device="cuda", dtype=torch.int32)
+        size = 1 << 24
+        ws = {"other device": lambda: torch.empty(size, dtype=torch.uint8),
+              "expanded": lambda: torch.empty(1, device="cuda", dtype=torch.uint8).expand(size),
+              "strided": lambda: torch.empty(size, 2, device="cuda", dtype=torch.uint8)[:, 0]}[bad]()
+        q, cache = torch.empty(2, 4, 64, **cuda), torch.empty(3, 2, 16, 64, **cuda)
+        with pytest.raises(ValueError, match="workspace"):
+            kda.attn_decode(q, cache, cache, torch.empty(2, 2, **i32), torch.empty(2, **i32), workspace=ws)
+        w = torch.empty(64, **cuda)
+        with pytest.raises(ValueError, match="workspace"):
+            kda.qk_norm_rope_bwd(q, q, q, q, w, w, workspace=ws)
