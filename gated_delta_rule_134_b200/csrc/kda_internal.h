@@ -93,6 +93,8 @@ struct RecurrenceArgs {
     long long wait_cycles = 1ll << 31;  // SM cycles that a wait within a cluster lasts at most: about a second
     int test_withhold = 0;              // fault injection: the first CTA of a cluster sends nothing
 };
+// Tokens of a sequence, of a packed batch on average (T and N reach 2^31 and 2^26: their sum leaves int).
+inline long long tokens_of(const RecurrenceArgs& a) { return a.cu_seqlens ? ((long long)a.T + a.N - 1) / a.N : a.T; }
 // Whether a wait gave up on the current device since the last call; clears it.
 cudaError_t recurrence_late(unsigned* flag);
 cudaError_t launch_recurrence_fwd(const RecurrenceArgs& a, cudaStream_t stream);

@@ -715,7 +715,7 @@ cudaError_t launch_scan(const RecurrenceArgs& a, cudaStream_t stream) {
     constexpr int CT = 8 * Pack<T>::V;
     const int slices = (a.D + CT - 1) / CT;
     const long long rows = (long long)a.N * slices;
-    const long long tokens = a.cu_seqlens ? (a.T + a.N - 1) / a.N : a.T;
+    const long long tokens = tokens_of(a);
     // CTAs of a cluster. From 75 rows on one: the rows alone fill the SMs (128 rows, T 8192 backward: 127 us, with two
     // 131). Below, as many as fit on the GPU at once, one an SM, where a cluster takes SMs of one GPC: six clusters of
     // sixteen (four rows, T 65536: 52 us, with eight 98), fourteen of eight (twelve rows, T 32768: 53 us, with sixteen 57),

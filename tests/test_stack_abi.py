@@ -162,3 +162,29 @@ def test_binding_refuses_workspaces_that_are_not_its_memory(bad):
         w = torch.empty(64, **cuda)
         with pytest.raises(ValueError, match="workspace"):
             kda.qk_norm_rope_bwd(q, q, q, q, w, w, workspace=ws)
+
+
+def test_tokens_of_the_longest_packed_batches(tmp_path):
+    """What the recurrence's plan goes by, compiled for the host: sequences of 2^30 tokens must not count as negative."""
+    import shutil
+    import subprocess
+
+    from gated_delta_rule_134_b200 import build
+    src, exe = tmp_path / "tokens.cpp", tmp_path / "tokens"
+    src.write_text("""#include <cstdio>
+#include "kda_internal.h"
+int main() {
+    const int cu = 0, sizes[][2] = {{1, 5}, {2, 5}, {2, 0x7fffffff}, {1 << 26, 0x7fffffff}};
+    for (auto& s : sizes) {
+        kda::RecurrenceArgs a{};
+        a.N = s[0]; a.T = s[1];
+        const long long dense = kda::tokens_of(a);
+        a.cu_seqlens = &cu;
+        std::printf("%lld %lld\\n", dense, kda::tokens_of(a));
+    }
+}
+""")
+    cuda = str(build.NVCC).rsplit("/bin/", 1)[0]
+    subprocess.run([shutil.which("g++") or "c++", "-std=c++17", "-I", build.INCLUDE, "-I", build.CSRC, "-I", cuda + "/include", str(src), "-o", str(exe)], check=True)
+    got = [tuple(map(int, line.split())) for line in subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.splitlines()]
+    assert got == [(5, 5), (5, 3), (0x7fffffff, 1 << 30), (0x7fffffff, 32)]
