@@ -508,7 +508,9 @@ def recurrence_fwd(log_alpha, x, h0=None, *, cu_seqlens=None, output_final_state
     log_alpha, x: [B,T,D], or packed [total_T,D] with cu_seqlens int32 [N+1];
     both float32 or both bfloat16. h0: [B or N,D] float32 or None (zero).
     Returns (h, h_T): h like x, h_T [B or N,D] float32 (None when
-    output_final_state is False). h may be x, h_T may be h0."""
+    output_final_state is False). h may be x, h_T may be h0. Tokens outside
+    every packed sequence are not written: an h made here holds anything
+    there."""
     import torch
     lib = load()
     N, T, D = _recurrence_sizes(log_alpha, cu_seqlens)
@@ -534,11 +536,14 @@ def recurrence_fwd(log_alpha, x, h0=None, *, cu_seqlens=None, output_final_state
     return h, h_T
 
 
-def recurrence_bwd(log_alpha, h, h0, dh, dh_T=None, *, cu_seqlens=None, want_dh0: bool = True, stream=None) -> dict:
+def recurrence_bwd(log_alpha, h, h0, dh, dh_T=None, *, cu_seqlens=None, want_dh0: bool = True, dx=None, dlog_alpha=None,
+                   stream=None) -> dict:
     """kda_recurrence_bwd: gradients of a loss with dL/dh = dh and dL/dh_T =
     dh_T ([B or N,D] float32 or None). log_alpha, h0, cu_seqlens as for
     recurrence_fwd, h its output. Returns dict dx, dlog_alpha, dh0 (None
-    unless want_dh0)."""
+    unless want_dh0). dx may be dh. Tokens outside every packed sequence are
+    not written: for a batch with such tokens give a dx and dlog_alpha that
+    hold zeros there."""
     import torch
     lib = load()
     N, T, D = _recurrence_sizes(log_alpha, cu_seqlens)
@@ -551,8 +556,13 @@ def recurrence_bwd(log_alpha, h, h0, dh, dh_T=None, *, cu_seqlens=None, want_dh0
         _need(h0, "h0", (N, D), torch.float32, dev)
     if dh_T is not None:
         _need(dh_T, "dh_T", (N, D), torch.float32, dev)
+    if dx is not None:
+        _need(dx, "dx", shape, dt, dev)
+    if dlog_alpha is not None:
+        _need(dlog_alpha, "dlog_alpha", shape, dt, dev)
     with _memory_of(stream):
-        g = {"dx": torch.empty_like(dh), "dlog_alpha": torch.empty_like(log_alpha),
+        g = {"dx": torch.empty_like(dh) if dx is None else dx,
+             "dlog_alpha": torch.empty_like(log_alpha) if dlog_alpha is None else dlog_alpha,
              "dh0": torch.empty(N, D, dtype=torch.float32, device=dev) if want_dh0 else None}
     with _on(dev):
         code = lib.kda_recurrence_bwd(_ptr(log_alpha), _ptr(h), _ptr(h0), _ptr(dh), _ptr(dh_T), _ptr(g["dx"]),

@@ -377,7 +377,8 @@ kda_status_t kda_recurrence_fwd(const void *log_alpha, const void *x, const floa
  *                     log_alpha takes h_{t-1} as it was rounded)
  *   d_h             : [N, T, D] or packed [T, D], dtype
  *   d_h_T           : [N, D] float; NULL means zero
- *   d_x, d_log_alpha: like x, dtype, written (d_x may equal d_h)
+ *   d_x, d_log_alpha: like x, dtype, written (d_x may equal d_h); tokens outside
+ *                     every packed sequence keep what both held before
  *   d_h0            : [N, D] float, written; NULL: not computed
  */
 kda_status_t kda_recurrence_bwd(const void *log_alpha, const void *h, const float *h0, const void *d_h,

@@ -346,3 +346,26 @@ def test_decays(cuda_lib, dtype):
     for got, bound, what in ((end, scan, "scan"), (grads["dh0"], scan, "backward"), (step, 2 * R.U, "step")):
         off = (got.cpu().double() / x.exp() - 1).abs()
         assert bool((off <= bound).all()), (what, float((off / R.U).max()))
+
+
+@pytest.mark.parametrize("D", [24, 25, 26])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_gradients_in_given_memory(cuda_lib, dtype, D):
+    """dx over dh; tokens of no sequence keep what dx and dlog_alpha held, before the first sequence and behind the last."""
+    log_alpha, x, g = draw((100, D), DT[dtype], 43)
+    cu = torch.tensor([7, 30, 30, 71], dtype=torch.int32).cuda()
+    h0, dT = (torch.randn(3, D, generator=g).cuda() for _ in range(2))
+    la, xd = log_alpha.cuda(), x.cuda()
+    h, _ = cuda_lib.recurrence_fwd(la, xd, h0, cu_seqlens=cu, h=torch.zeros_like(xd))
+    want = cuda_lib.recurrence_bwd(la, h, h0, xd, dT, cu_seqlens=cu)
+    dx, dla = xd.clone(), torch.full_like(la, 7.0)
+    got = cuda_lib.recurrence_bwd(la, h, h0, dx, dT, cu_seqlens=cu, dx=dx, dlog_alpha=dla)
+    assert got["dx"] is dx and got["dlog_alpha"] is dla and torch.equal(got["dh0"], want["dh0"])
+    for name, before in (("dx", xd), ("dlog_alpha", torch.full_like(la, 7.0))):
+        assert torch.equal(got[name][7:71], want[name][7:71]), name
+        for outside in (slice(0, 7), slice(71, 100)):
+            assert torch.equal(got[name][outside], before[outside]), name
+    with pytest.raises(ValueError, match="dx: expected"):
+        cuda_lib.recurrence_bwd(la, h, h0, xd, dT, cu_seqlens=cu, dx=dx[:50])
+    with pytest.raises(ValueError, match="dlog_alpha: expected"):
+        cuda_lib.recurrence_bwd(la, h, h0, xd, dT, cu_seqlens=cu, dlog_alpha=dla.double())
