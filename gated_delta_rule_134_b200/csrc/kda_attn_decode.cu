@@ -9,14 +9,17 @@
 // key-value head and 4 d flop per query head, so the products run on warp MMAs
 // (16 positions x 8 or 16 query heads; fewer heads leave columns empty, which
 // costs nothing while the loads set the pace). 64 rows of 256 to 16384 positions,
-// 8 key-value heads, d 128, bf16: 167-171 us, 0.94-0.96 of the measured copy
-// bandwidth, the tensor pipe 9 % busy.
+// 8 key-value heads, d 128, bf16: 170-172 us, 0.93-0.94 of the measured copy
+// bandwidth, the tensor pipe 13 % busy.
 //
 // Split: the positions of all (sequence, key-value head, block of 16 query
 // heads) are cut into tiles of 16, and the list of all tiles is cut into equal
 // contiguous ranges, one per warp ("worker"), whatever the lengths are: a
-// batch of one long and many short contexts loads every SM alike. (To begin and
-// to end a pair costs as much as some tiles, so each pair counts kBegin more.)
+// batch of one long and many short contexts loads every SM alike in this kernel.
+// (To begin and to end a pair costs as much as some tiles, so each pair counts
+// kBegin more.) The join's warps go by the number of pairs, so one very long
+// context among many has its many pieces joined by one warp a head (131072
+// positions and 63 rows of 256: 124 us, 0.75 of the copy bandwidth).
 // Workers find their range from seq_lens on the device. A worker that holds all
 // tiles of a pair writes its output; else it leaves (m, l, O) in the workspace,
 // where it has two places: 0 for a range that continues a pair, 1 for one that begins a

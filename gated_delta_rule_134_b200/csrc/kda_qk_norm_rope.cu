@@ -12,8 +12,8 @@
 // unnormalised, in the lane rot/16 away (halves). A group takes up to `chunk`
 // heads of one token, so that the token's row of the tables, with the weight
 // multiplied in, is read once for them all. 32768 tokens x 64 heads of 128, bf16:
-// 158 us (1.05 of the measured copy bandwidth); backward of 8192 x 40: 49 us (0.80,
-// bound by its instructions and by the second kernel that sums the weights).
+// 158 us (1.05 of the measured copy bandwidth); backward of 8192 x 40: 49-51 us
+// (0.77-0.80, bound by its instructions and by the second kernel that sums the weights).
 #include <algorithm>
 #include <type_traits>
 

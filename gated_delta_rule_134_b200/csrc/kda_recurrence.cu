@@ -20,9 +20,9 @@
 //   3. walks the parts before its own, which gives the state that enters each of
 //      its groups, and leaves these in shared memory;
 //   4. runs its tokens again from the state that enters them and writes them.
-// B4 T8192 D4096 bf16 takes 132-135 us (0.93 of the measured copy bandwidth), the
-// backward pass of B2 111-114 us (0.92). Where rows are few, a cluster of CTAs
-// shares one (recurrence_cluster_kernel). The order of every product and sum is
+// B4 T8192 D4096 bf16 takes 134-139 us by the box (0.90-0.93 of the measured copy
+// bandwidth), the backward pass of B2 114-117 us (0.89-0.91). Where rows are few, a
+// cluster of CTAs shares one (recurrence_cluster_kernel). The order of every product and sum is
 // fixed by the sizes alone.
 #include "kda_async.cuh"
 #include "kda_common.cuh"
@@ -431,7 +431,9 @@ struct Walk {
 };
 
 // The k-th longest of N <= THREADS packed sequences: CTAs are given out in this order, so that no long sequence begins
-// when the others are done (nine sequences of 0 to 3400 tokens, D 2048: 46.7 us in the order they lie, 40.8 so).
+// when the others are done (nine sequences of 0 to 3400 tokens, D 2048: 46.7 us in the order they lie, 40.8 so). Every CTA
+// counts for itself, N steps: many short sequences lose more than they gain (256 of 64 tokens, D 4096: 329 us, the same
+// tokens as a dense batch 137).
 template <int THREADS> __device__ __forceinline__ int longest(const RecurrenceArgs& a, int k, int* scratch) {
     const int i = threadIdx.x;
     long long begin;
@@ -717,10 +719,11 @@ cudaError_t launch_scan(const RecurrenceArgs& a, cudaStream_t stream) {
     const long long rows = (long long)a.N * slices;
     const long long tokens = tokens_of(a);
     // CTAs of a cluster. From 75 rows on one: the rows alone fill the SMs (128 rows, T 8192 backward: 127 us, with two
-    // 131). Below, as many as fit on the GPU at once, one an SM, where a cluster takes SMs of one GPC: six clusters of
-    // sixteen (four rows, T 65536: 52 us, with eight 98), fourteen of eight (twelve rows, T 32768: 53 us, with sixteen 57),
-    // thirty-four of four (32 rows, T 16384: 52 us, with two 89), else two; 15 and 16 rows take clusters of sixteen in two
-    // rounds (T 32768: 82 us, with four 97). No more than the tokens give tiles to.
+    // 131). Below, about as many as fit on the GPU at once, one an SM, where a cluster takes SMs of one GPC (one B200 says
+    // that it holds 7 of sixteen, 15 of eight, 33 of four; it depends on which SMs a GPU has): six clusters of sixteen
+    // (four rows, T 65536: 52 us, with eight 98), fourteen of eight (twelve rows, T 32768: 53 us, with sixteen 57),
+    // thirty-four of four (32 rows, T 16384: 52 us, with two 89), else two; 15 and 16 rows take clusters of sixteen in
+    // three rounds (T 32768: 82 us, with four 97). No more than the tokens give tiles to.
     const int most = rows <= 6 ? 16 : rows <= 14 ? 8 : rows <= 16 ? 16 : rows <= 34 ? 4 : rows < 75 ? 2 : 1;
     int size = 1;
     while (size < most && (long long)size * (256 / 8) * cluster_tokens<T, ALIGN, BWD>() < tokens) size *= 2;
