@@ -20,7 +20,7 @@
 //   3. walks the parts before its own, which gives the state that enters each of
 //      its groups, and leaves these in shared memory;
 //   4. runs its tokens again from the state that enters them and writes them.
-// B4 T8192 D4096 bf16 takes 134-139 us by the box (0.90-0.93 of the measured copy
+// B4 T8192 D4096 bf16 takes 134-139 us, by the B200 (0.90-0.93 of the measured copy
 // bandwidth), the backward pass of B2 114-117 us (0.89-0.91). Where rows are few, a
 // cluster of CTAs shares one (recurrence_cluster_kernel). The order of every product and sum is
 // fixed by the sizes alone.
